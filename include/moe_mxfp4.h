@@ -326,8 +326,8 @@ moe_status moe_device_status(void* ws, void* stream);
 /* Static description of a status code. */
 const char* moe_status_string(moe_status status);
 
-/* Number of kernels the last successful moe_forward / moe_route call on this host
- * thread launched (for launch accounting in benchmarks). */
+/* Number of kernels the last successful launching call (moe_forward, moe_route, a product, a
+ * norm) on this host thread launched (for launch accounting in benchmarks). */
 int32_t moe_last_launch_count(void);
 
 /* moe_forward for callers that cannot allocate device memory: it takes no workspace and
@@ -357,11 +357,123 @@ moe_status moe_forward_no_alloc(const moe_dims* dims, int32_t T, const uint16_t*
                                 const uint8_t* w1_scales, const uint8_t* w2_codes, const uint8_t* w2_scales,
                                 uint16_t* y, int32_t* status_out, void* stream);
 
+/* ---------------------------------------------------- 16-bit products and norms, with gradients
+ * What a training step of the layer, or the dense blocks around it, needs beside the MXFP4
+ * forward: the row norm, the matrix product with bias, activation and residual, and the same
+ * product grouped by expert, each with its backward pass.  Extensions: the pages state the
+ * forward layer only ("From GPT-2 to gpt-oss" describes the dense block it replaces: norm,
+ * linears, activation).
+ *
+ * Rows may be strided: ld* is the distance between rows in elements (at least the row's
+ * length).  The products take 16-bit tensors (bf16 or fp16, all tensors of a call alike) with
+ * K and N multiples of 8, ld* multiples of 8 and 16-byte aligned pointers; sums are fp32,
+ * biases and their gradients fp32.  W and z are contiguous.  Weight-gradient results do not
+ * depend on scheduling: no atomics, fixed summation order.  Calls keep nothing between them;
+ * the backward calls' workspace is scratch whose contents need not be kept or cleared, and
+ * calls that may overlap on the GPU need workspaces of their own.
+ * status_word: optional device int32 (NULL to skip), readable with moe_device_status() if it
+ * is 16-byte aligned: MOE_ERR_TIMEOUT (a pipeline wait gave up), MOE_ERR_INVALID_ARG (offsets
+ * out of range or decreasing; no address outside the buffers is touched, the results are
+ * unspecified). */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dtype;
+
+/* Norm of a row.  RMS: the layer's RMSNorm (no mean, no bias).  LAYER: layer norm. */
+typedef enum { MOE_NORM_RMS = 0, MOE_NORM_LAYER = 1 } moe_norm_kind;
+
+/* Activation f of a product.  GELU is z (1 + erf(z / sqrt 2)) / 2, GELU_TANH its tanh form.
+ * SWIGLU: W holds N/2 gate rows, then the N/2 matching up rows (N a multiple of 16), and
+ * y = silu(min(g, limit)) * clamp(u, -limit, limit) has N/2 columns: the experts' activation. */
+typedef enum {
+  MOE_FN_NONE = 0,
+  MOE_FN_RELU = 1,
+  MOE_FN_GELU = 2,
+  MOE_FN_GELU_TANH = 3,
+  MOE_FN_SILU = 4,
+  MOE_FN_SWIGLU = 5
+} moe_fn;
+
+typedef struct {
+  int32_t K;      /* input features (columns of x), 8 .. 65536                       */
+  int32_t N;      /* rows of W per expert, 8 .. 131072                               */
+  int32_t E;      /* experts, 1 .. 256 (moe_linear: 1)                               */
+  int32_t dtype;  /* MOE_DTYPE_BF16 or MOE_DTYPE_F16                                 */
+  int32_t fn;     /* a moe_fn value                                                  */
+  float limit;    /* SWIGLU: the clamp (> 0); other activations ignore it            */
+} moe_linear_dims;
+
+/* y = (x - m) * r * w + b per row of x [T][d]; m = mean(x) (RMS: 0), r = 1 / sqrt(mean((x -
+ * m)^2) + eps).  x and y share dtype (any moe_dtype); w, b fp32 [d]; b is for LAYER only and
+ * may be NULL.  mean, rstd: optional fp32 [T] outputs for the backward pass (mean: LAYER).
+ * d from 1 to 65536, any strides; 16-byte aligned pointers and strides with d a multiple of
+ * 16 bytes take the vectorised path.  y may be x itself (same stride), else not overlap it.
+ * Errors: MOE_ERR_INVALID_ARG (T < 0, d <= 0, a null pointer or one not aligned to its
+ * element, ld below d, bad eps or enum, b with RMS), MOE_ERR_UNSUPPORTED_SHAPE (d above 65536,
+ * T above 2^24), MOE_ERR_DEVICE, MOE_ERR_CUDA. */
+moe_status moe_norm(int32_t kind, int32_t dtype, int32_t T, int32_t d, const void* x, int64_t ldx, const float* w,
+                    const float* b, float eps, void* y, int64_t ldy, float* mean, float* rstd, void* stream);
+
+/* Backward pass of moe_norm, from its x, w and statistics:  xh = (x - mean) * rstd,
+ *   g = dy * w,  dx = rstd * (g - xh * mean(g * xh) - [LAYER] mean(g)) [+ dres],
+ *   dw = sum over rows of dy * xh,  db = sum over rows of dy   (fp32 [d], NULL to skip)
+ * dres [T][d]: an optional gradient added to dx in the same pass (the residual stream's).  dx
+ * may be dy, x or dres itself (same stride).  ws: moe_norm_workspace_bytes(T, d) bytes, needed
+ * with dw or db.  T = 0 writes zeros to dw and db.  Errors: as moe_norm, MOE_ERR_WORKSPACE. */
+moe_status moe_norm_backward(int32_t kind, int32_t dtype, int32_t T, int32_t d, const void* dy, int64_t lddy,
+                             const void* x, int64_t ldx, const float* w, const float* mean, const float* rstd,
+                             const void* dres, int64_t lddres, void* dx, int64_t lddx, float* dw, float* db, void* ws,
+                             size_t ws_bytes, void* stream);
+size_t moe_norm_workspace_bytes(int32_t T, int32_t d);
+
+/* z = x W^T + bias, y = f(z) + residual for x [M][K], W [N][K], bias fp32 [N] or NULL;
+ * y [M][N] (SWIGLU: [M][N/2]); residual of y's shape, or NULL.  z [M][N] (contiguous, NULL to
+ * skip) receives the pre-activation, rounded to dtype, for the backward pass.  y may be the
+ * residual itself (same stride); otherwise outputs may not overlap inputs.  M = 0 returns
+ * MOE_OK and launches nothing.
+ * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointer, ld not a multiple of 8 or below the
+ * row, bad enum, limit not finite or not positive with SWIGLU), MOE_ERR_UNSUPPORTED_SHAPE (K
+ * or N not a multiple of 8, N not of 16 with SWIGLU, out of range, E != 1, M above 2^24),
+ * MOE_ERR_DEVICE, MOE_ERR_CUDA. */
+moe_status moe_linear(const moe_linear_dims* dims, int32_t M, const void* x, int64_t ldx, const void* w,
+                      const float* bias, const void* residual, int64_t ldr, void* y, int64_t ldy, void* z,
+                      int32_t* status_word, void* stream);
+
+/* Backward pass of moe_linear from dy (of y's shape), x, w and the z of the forward pass (fn
+ * != NONE; NULL otherwise):  dz = dy * f'(z) (a clamp passes the gradient up to and at its
+ * bound; RELU at 0: 0),  dx = dz W [M][K],  dw = dz^T x [N][K],  db = column sums of dz [N]
+ * fp32.  The residual's gradient is dy itself.  dx, dw, db: NULL to skip.  dz enters the
+ * products rounded to dtype (the tensor cores' operand type); db sums it unrounded.
+ * ws: moe_linear_workspace_bytes(dims, M) bytes, 16-byte aligned.  M = 0 writes zeros to dw
+ * and db.  x is needed for dw only, w for dx only.  Errors: as moe_linear, MOE_ERR_WORKSPACE. */
+moe_status moe_linear_backward(const moe_linear_dims* dims, int32_t M, const void* dy, int64_t lddy, const void* x,
+                               int64_t ldx, const void* w, const void* z, void* dx, int64_t lddx, void* dw, float* db,
+                               void* ws, size_t ws_bytes, int32_t* status_word, void* stream);
+
+/* moe_linear grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of x [P][K] take W[e]
+ * ([E][N][K]) and bias[e] ([E][N]).  offsets int32 [E + 1] (device), non-decreasing within
+ * [0, P], as moe_route writes them; an expert may have no rows.  Rows that no expert covers
+ * are left as they were in y and z.  P = 0 launches nothing.  Errors: as moe_linear. */
+moe_status moe_grouped_linear(const moe_linear_dims* dims, int32_t P, const void* x, int64_t ldx, const void* w,
+                              const int32_t* offsets, const float* bias, void* y, int64_t ldy, void* z,
+                              int32_t* status_word, void* stream);
+
+/* Backward pass of moe_grouped_linear: as moe_linear_backward per expert, dw [E][N][K] and db
+ * [E][N] (zeros for an expert without rows); rows of dx that no expert covers are left as they
+ * were. */
+moe_status moe_grouped_linear_backward(const moe_linear_dims* dims, int32_t P, const void* dy, int64_t lddy,
+                                       const void* x, int64_t ldx, const void* w, const int32_t* offsets,
+                                       const void* z, void* dx, int64_t lddx, void* dw, float* db, void* ws,
+                                       size_t ws_bytes, int32_t* status_word, void* stream);
+
+/* Workspace of the two backward calls for `rows` rows (M or P); 0 for unsupported dims. */
+size_t moe_linear_workspace_bytes(const moe_linear_dims* dims, int32_t rows);
+
 /* Test hook for the device-side failure path.  With enable != 0, the next moe_forward
  * (or moe_forward_timed) call on this host thread launches its gate_up kernel with one pipeline arrival withheld in its first CTA: that CTA's bounded
  * wait expires after about 2 s, the CTA drains its copies, frees its tensor memory and
  * exits, and the workspace status word records MOE_ERR_TIMEOUT (y of that call is then
- * unspecified).  The hook clears itself after that call; nothing faults or hangs. */
+ * unspecified).  The product calls (moe_linear, moe_grouped_linear and their backward passes)
+ * take the hook in the same way, in their first product kernel, and record the timeout in their
+ * status_word.  The hook clears itself after that call; nothing faults or hangs. */
 void moe_debug_inject_timeout(int32_t enable);
 
 #ifdef __cplusplus

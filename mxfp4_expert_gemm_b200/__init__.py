@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -44,6 +45,10 @@ MOE_WEIGHT_PLAIN = 0
 MOE_WEIGHT_GATE_UP = 1
 ROLES = {"plain": MOE_WEIGHT_PLAIN, "down": MOE_WEIGHT_PLAIN, "gate_up": MOE_WEIGHT_GATE_UP}
 
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}      # moe_dtype
+NORM_KINDS = {"rms": 0, "layer": 1}                                     # moe_norm_kind
+FNS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "swiglu": 5}   # moe_fn
+
 
 class MoeError(RuntimeError):
     def __init__(self, status: int, what: str):
@@ -55,6 +60,11 @@ class moe_dims(ctypes.Structure):
     _fields_ = [("d", ctypes.c_int32), ("I", ctypes.c_int32), ("E", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("block", ctypes.c_int32), ("rms_eps", ctypes.c_float), ("swiglu_limit", ctypes.c_float),
                 ("path", ctypes.c_int32), ("act_format", ctypes.c_int32)]
+
+
+class moe_linear_dims(ctypes.Structure):
+    _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("E", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("fn", ctypes.c_int32), ("limit", ctypes.c_float)]
 
 
 def make_dims(d: int, I: int, E: int, top_k: int, rms_eps: float = 1e-5, swiglu_limit: float = 7.0,
@@ -140,6 +150,23 @@ def load_library(path: str):
     L.moe_forward_host.restype = ctypes.c_int
     L.moe_host_chunk_tokens.argtypes = [dp, i32]
     L.moe_host_chunk_tokens.restype = i32
+    i64, lp = ctypes.c_int64, ctypes.POINTER(moe_linear_dims)
+    L.moe_norm.argtypes = [i32, i32, i32, i32, vp, i64, vp, vp, ctypes.c_float, vp, i64, vp, vp, vp]
+    L.moe_norm.restype = ctypes.c_int
+    L.moe_norm_backward.argtypes = [i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, i64, vp, vp, vp, sz, vp]
+    L.moe_norm_backward.restype = ctypes.c_int
+    L.moe_norm_workspace_bytes.argtypes = [i32, i32]
+    L.moe_norm_workspace_bytes.restype = sz
+    L.moe_linear.argtypes = [lp, i32, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp, vp]
+    L.moe_linear.restype = ctypes.c_int
+    L.moe_linear_backward.argtypes = [lp, i32, vp, i64, vp, i64, vp, vp, vp, i64, vp, vp, vp, sz, vp, vp]
+    L.moe_linear_backward.restype = ctypes.c_int
+    L.moe_grouped_linear.argtypes = [lp, i32, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp]
+    L.moe_grouped_linear.restype = ctypes.c_int
+    L.moe_grouped_linear_backward.argtypes = [lp, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, vp, sz, vp, vp]
+    L.moe_grouped_linear_backward.restype = ctypes.c_int
+    L.moe_linear_workspace_bytes.argtypes = [lp, i32]
+    L.moe_linear_workspace_bytes.restype = sz
     L.moe_debug_inject_timeout.argtypes = [i32]
     L.moe_debug_inject_timeout.restype = None
     L.moe_last_launch_count.argtypes = []
@@ -452,3 +479,253 @@ def moe_forward_no_alloc(dims: moe_dims, x, norm_w, router_w, router_b, w1_codes
 def moe_debug_inject_timeout(enable: bool = True) -> None:
     """Test hook: the next tensor-core forward on this thread times out in one CTA (see the header)."""
     lib().moe_debug_inject_timeout(1 if enable else 0)
+
+
+# ----------------------------------------------------------- norms and 16-bit products, with gradients
+def _rows(t: torch.Tensor, dtype, name, device, shape=None) -> int:
+    """Row stride of a [rows, columns] tensor whose columns are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: a CUDA tensor is required")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape) if shape else '[rows, columns]'}")
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols != 1:
+        raise ValueError(f"{name}: the columns of a row must be contiguous")
+    if rows <= 1 and ld < cols:
+        return cols
+    return ld
+
+
+def _flat(t, dtype, name, device, shape):
+    """A contiguous tensor of the given shape, or None."""
+    if t is None:
+        return None
+    _need(t, dtype, name, shape)
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _here(t, name) -> torch.device:
+    """The device of a call's first tensor, which has to be the current one."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: a CUDA tensor is required")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _raw_stream(stream) -> int:
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _status(status_word, device):
+    if status_word is None:
+        return None
+    _need(status_word, torch.int32, "status_word")
+    if status_word.device != device:
+        raise ValueError(f"status_word: on {status_word.device}, expected {device}")
+    return status_word.data_ptr()
+
+
+def _workspace(ws, nbytes, device):
+    """(pointer, bytes) of a caller's workspace, or of one taken from torch's allocator."""
+    if ws is None:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    elif ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on {device} is required")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _norm_kind(kind) -> int:
+    if kind not in NORM_KINDS:
+        raise ValueError(f"kind: {kind!r}, expected one of {sorted(NORM_KINDS)}")
+    return NORM_KINDS[kind]
+
+
+def moe_norm(x, w, b=None, kind="rms", eps=1e-5, y=None, want_stats=False, stream=None):
+    """y [T, d] = RMSNorm(x) * w (kind "rms") or LayerNorm(x) * w + b (kind "layer"); bf16, fp16
+    or fp32 rows, fp32 w and b.  With want_stats: (y, mean, rstd) for moe_norm_backward (mean is
+    None for "rms")."""
+    dev = _here(x, "x")
+    if x.dtype not in DTYPES:
+        raise TypeError(f"x: dtype {x.dtype}")
+    k = _norm_kind(kind)
+    ldx = _rows(x, x.dtype, "x", dev)
+    T, d = x.shape
+    if y is None:
+        y = torch.empty((T, d), dtype=x.dtype, device=dev)
+    mean = rstd = None
+    if want_stats:
+        stats = torch.empty((2, T), dtype=torch.float32, device=dev)
+        rstd, mean = stats[0], stats[1] if k == 1 else None
+    _check(lib().moe_norm(k, DTYPES[x.dtype], T, d, x.data_ptr(), ldx, _flat(w, torch.float32, "w", dev, (d,)),
+                          _flat(b, torch.float32, "b", dev, (d,)), eps, y.data_ptr(),
+                          _rows(y, x.dtype, "y", dev, x.shape), None if mean is None else mean.data_ptr(),
+                          None if rstd is None else rstd.data_ptr(), _raw_stream(stream)), "moe_norm")
+    return (y, mean, rstd) if want_stats else y
+
+
+def moe_norm_workspace_bytes(T: int, d: int) -> int:
+    return lib().moe_norm_workspace_bytes(T, d)
+
+
+def moe_norm_backward(dy, x, w, mean, rstd, kind="rms", dres=None, dx=None, need_dw=True, need_db=None, ws=None,
+                      stream=None):
+    """(dx, dw, db) of moe_norm, with dres (a gradient of dx's shape) added to dx in the same pass.
+    dw and db are fp32 [d]; db defaults to kind == "layer" and is None when not asked for."""
+    dev = _here(x, "x")
+    if x.dtype not in DTYPES:
+        raise TypeError(f"x: dtype {x.dtype}")
+    k = _norm_kind(kind)
+    ldx = _rows(x, x.dtype, "x", dev)
+    T, d = x.shape
+    if need_db is None:
+        need_db = k == 1
+    lddy = _rows(dy, x.dtype, "dy", dev, x.shape)
+    lddres = 0 if dres is None else _rows(dres, x.dtype, "dres", dev, x.shape)
+    if dx is None:
+        dx = torch.empty((T, d), dtype=x.dtype, device=dev)
+    dw = torch.empty(d, dtype=torch.float32, device=dev) if need_dw else None
+    db = torch.empty(d, dtype=torch.float32, device=dev) if need_db else None
+    ws_ptr, ws_bytes = None, 0
+    if need_dw or need_db:
+        ws, ws_ptr, ws_bytes = _workspace(ws, moe_norm_workspace_bytes(T, d), dev)
+    _check(lib().moe_norm_backward(k, DTYPES[x.dtype], T, d, dy.data_ptr(), lddy, x.data_ptr(), ldx,
+                                   _flat(w, torch.float32, "w", dev, (d,)),
+                                   _flat(mean, torch.float32, "mean", dev, (T,)),
+                                   _flat(rstd, torch.float32, "rstd", dev, (T,)),
+                                   None if dres is None else dres.data_ptr(), lddres, dx.data_ptr(),
+                                   _rows(dx, x.dtype, "dx", dev, x.shape), None if dw is None else dw.data_ptr(),
+                                   None if db is None else db.data_ptr(), ws_ptr, ws_bytes, _raw_stream(stream)),
+           "moe_norm_backward")
+    return dx, dw, db
+
+
+@functools.lru_cache(maxsize=256)
+def make_linear_dims(K: int, N: int, E: int = 1, dtype=torch.bfloat16, fn: str = "none",
+                     limit: float = 7.0) -> moe_linear_dims:
+    if fn not in FNS:
+        raise ValueError(f"fn: {fn!r}, expected one of {sorted(FNS)}")
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError(f"the products take bf16 or fp16 tensors, not {dtype}")
+    return moe_linear_dims(K, N, E, DTYPES[dtype], FNS[fn], limit)
+
+
+def moe_linear_workspace_bytes(dims: moe_linear_dims, rows: int) -> int:
+    return lib().moe_linear_workspace_bytes(ctypes.byref(dims), rows)
+
+
+def _product_dims(x, w, grouped, fn, limit):
+    """(device, row stride of x, dims) of a product's x [rows, K] and w [N, K] ([E, N, K])."""
+    dev = _here(x, "x")
+    ldx = _rows(x, x.dtype, "x", dev)
+    want = 3 if grouped else 2
+    if not isinstance(w, torch.Tensor) or w.dim() != want or w.shape[-1] != x.shape[1]:
+        raise ValueError(f"w: a tensor {'[E, N, K]' if grouped else '[N, K]'} with K = {x.shape[1]} is required")
+    _flat(w, x.dtype, "w", dev, w.shape)
+    return dev, ldx, make_linear_dims(x.shape[1], w.shape[-2], w.shape[0] if grouped else 1, x.dtype, fn, limit)
+
+
+def _forward_product(what, x, w, offsets, bias, fn, limit, residual, y, z, want_z, status_word, stream):
+    grouped = offsets is not None
+    dev, ldx, dims = _product_dims(x, w, grouped, fn, limit)
+    rows, N = x.shape[0], dims.N
+    No = N // 2 if fn == "swiglu" else N
+    if y is None:
+        y = torch.empty((rows, No), dtype=x.dtype, device=dev)
+    if want_z and z is None:
+        z = torch.empty((rows, N), dtype=x.dtype, device=dev)
+    ldy = _rows(y, x.dtype, "y", dev, (rows, No))
+    zp = _flat(z, x.dtype, "z", dev, (rows, N))
+    bp = _flat(bias, torch.float32, "bias", dev, (dims.E, N) if grouped else (N,))
+    sp = _status(status_word, dev)
+    if grouped:
+        op = _flat(offsets, torch.int32, "offsets", dev, (dims.E + 1,))
+        st = lib().moe_grouped_linear(ctypes.byref(dims), rows, x.data_ptr(), ldx, w.data_ptr(), op, bp, y.data_ptr(),
+                                      ldy, zp, sp, _raw_stream(stream))
+    else:
+        ldr = 0 if residual is None else _rows(residual, x.dtype, "residual", dev, (rows, No))
+        st = lib().moe_linear(ctypes.byref(dims), rows, x.data_ptr(), ldx, w.data_ptr(), bp,
+                              None if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, zp, sp,
+                              _raw_stream(stream))
+    _check(st, what)
+    return (y, z) if want_z else y
+
+
+def _backward_product(what, dy, x, w, offsets, z, fn, limit, dx, dw, need_dx, need_dw, need_db, ws, status_word,
+                      stream):
+    grouped = offsets is not None
+    dev, ldx, dims = _product_dims(x, w, grouped, fn, limit)
+    rows, K, N = x.shape[0], dims.K, dims.N
+    lddy = _rows(dy, x.dtype, "dy", dev, (rows, N // 2 if fn == "swiglu" else N))
+    if fn != "none" and z is None:
+        raise ValueError(f"z: the forward pass's pre-activation is required with fn={fn!r}")
+    zp = _flat(z, x.dtype, "z", dev, (rows, N)) if fn != "none" else None
+    need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
+    if need_dx and dx is None:
+        dx = torch.empty((rows, K), dtype=x.dtype, device=dev)
+    if need_dw and dw is None:
+        dw = torch.empty(w.shape, dtype=x.dtype, device=dev)
+    lddx = _rows(dx, x.dtype, "dx", dev, (rows, K)) if need_dx else 0
+    dwp = _flat(dw, x.dtype, "dw", dev, w.shape) if need_dw else None
+    db = torch.empty(w.shape[:-1], dtype=torch.float32, device=dev) if need_db else None
+    ws_ptr, ws_bytes = None, 0
+    if fn != "none" or need_db:
+        ws, ws_ptr, ws_bytes = _workspace(ws, moe_linear_workspace_bytes(dims, rows), dev)
+    common = (zp, dx.data_ptr() if need_dx else None, lddx, dwp, db.data_ptr() if need_db else None, ws_ptr, ws_bytes,
+              _status(status_word, dev), _raw_stream(stream))
+    if grouped:
+        op = _flat(offsets, torch.int32, "offsets", dev, (dims.E + 1,))
+        st = lib().moe_grouped_linear_backward(ctypes.byref(dims), rows, dy.data_ptr(), lddy, x.data_ptr(), ldx,
+                                               w.data_ptr(), op, *common)
+    else:
+        st = lib().moe_linear_backward(ctypes.byref(dims), rows, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(),
+                                       *common)
+    _check(st, what)
+    return dx if need_dx else None, dw if need_dw else None, db
+
+
+def moe_linear(x, w, bias=None, fn="none", limit=7.0, residual=None, y=None, z=None, want_z=False, status_word=None,
+               stream=None):
+    """y = f(x w^T + bias) + residual for x [M, K], w [N, K] (bf16 or fp16), bias fp32 [N]; fn one
+    of "none", "relu", "gelu", "gelu_tanh", "silu", "swiglu" (w then holds N/2 gate rows and the N/2
+    matching up rows, and y has N/2 columns).  With want_z: (y, z), z [M, N] the pre-activation for
+    moe_linear_backward."""
+    return _forward_product("moe_linear", x, w, None, bias, fn, limit, residual, y, z, want_z, status_word, stream)
+
+
+def moe_linear_backward(dy, x, w, z=None, fn="none", limit=7.0, dx=None, dw=None, need_dx=True, need_dw=True,
+                        need_db=False, ws=None, status_word=None, stream=None):
+    """(dx, dw, db) of moe_linear (None for those not asked for); db is fp32 [N].  The residual's
+    gradient is dy itself.  ws: moe_linear_workspace_bytes of scratch (taken from torch's allocator
+    when None)."""
+    return _backward_product("moe_linear_backward", dy, x, w, None, z, fn, limit, dx, dw, need_dx, need_dw, need_db,
+                             ws, status_word, stream)
+
+
+def moe_grouped_linear(x, w, offsets, bias=None, fn="none", limit=7.0, y=None, z=None, want_z=False, status_word=None,
+                       stream=None):
+    """moe_linear grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of x [P, K] take w[e] of
+    w [E, N, K] and bias[e] of bias [E, N]; offsets int32 [E + 1], as moe_route returns them.  Rows
+    that no expert covers are left as they were in y and z (unset in tensors made here)."""
+    if offsets is None:
+        raise TypeError("offsets: a CUDA tensor is required")
+    return _forward_product("moe_grouped_linear", x, w, offsets, bias, fn, limit, None, y, z, want_z, status_word,
+                            stream)
+
+
+def moe_grouped_linear_backward(dy, x, w, offsets, z=None, fn="none", limit=7.0, dx=None, dw=None, need_dx=True,
+                                need_dw=True, need_db=False, ws=None, status_word=None, stream=None):
+    """(dx, dw, db) of moe_grouped_linear: dw [E, N, K] and db fp32 [E, N] are zero for an expert
+    without rows; rows of dx that no expert covers are left as they were (unset in a tensor made
+    here)."""
+    if offsets is None:
+        raise TypeError("offsets: a CUDA tensor is required")
+    return _backward_product("moe_grouped_linear_backward", dy, x, w, offsets, z, fn, limit, dx, dw, need_dx, need_dw,
+                             need_db, ws, status_word, stream)

@@ -1,0 +1,83 @@
+// PTX of the 16-bit products: tcgen05 kind::f16 with operands of either major order, and
+// rank-3 TMA tile loads.  Complements sm100_ptx.cuh.
+#pragma once
+
+#include "sm100_ptx.cuh"
+
+namespace moe {
+namespace ptx {
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::
+          "r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Instruction descriptor of kind::f16: fp16 or bf16 A and B, fp32 D; a_mn / b_mn: the operand
+// is MN-major (its rows in shared memory run along M or N) instead of K-major.
+__host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N, bool a_mn, bool b_mn) {
+  return (1u << 4)                                        // D format: f32
+         | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10)  // A, B format
+         | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16)
+         | ((uint32_t)(N >> 3) << 17)                     // N / 8
+         | ((uint32_t)(M >> 4) << 24);                    // M / 16
+}
+
+// SMEM descriptor of an MN-major operand laid out by 128-byte-swizzled loads of
+// [64 k][64 mn] boxes: rows of 128 bytes along MN, 8-k groups 1024 bytes apart, the next 64
+// values of MN one box (8192 bytes) on.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(const void* tile) {
+  const uint64_t addr = smem_u32(tile);
+  uint64_t d = (addr & 0x3FFFFull) >> 4;   // start address (16-byte units)
+  d |= (uint64_t)(8192 >> 4) << 16;        // leading byte offset: next 64 values of MN
+  d |= (uint64_t)(1024 >> 4) << 32;        // stride byte offset: next 8 values of K
+  d |= 1ull << 46;                          // descriptor version (sm_100)
+  d |= 2ull << 61;                          // 128-byte swizzle
+  return d;
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T over one 16-wide K block, kind::f16, one CTA.
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// As mma_f16_ss, over a CTA pair (M = 256: 128 rows of A and half of B's rows in each CTA).
+__device__ __forceinline__ void mma_f16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Rank-3 tile load into this CTA's shared memory completing on the pair leader's barrier
+// (`bar_cluster_addr`: the barrier's cluster-window address).  No multicast.
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map, int32_t c0, int32_t c1, int32_t c2,
+                                                 uint32_t bar_cluster_addr) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+      "%4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// Load from the shared memory of a CTA of the cluster (cluster-window address).
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+}  // namespace ptx
+}  // namespace moe

@@ -7,7 +7,7 @@
 #include <cstring>
 #include <vector>
 
-#include "moe_internal.cuh"
+#include "moe_linear.cuh"
 
 namespace {
 
@@ -229,6 +229,22 @@ thread_local HostEvents g_host_events;
 
 namespace moe {
 moe_status validate_dims(const moe_dims* dims, int32_t T) { return check_dims(dims, T); }
+moe_status device_status() { return check_device(); }
+void note_launches(int32_t n) { g_last_launches = n; }
+int32_t take_injected_timeout() {
+  const int32_t v = g_inject_timeout;
+  g_inject_timeout = 0;
+  return v;
+}
+int multiprocessors() {
+  static std::atomic<int> count[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < 64 && (n = count[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev < 64) count[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
 }  // namespace moe
 
 extern "C" {

@@ -1,0 +1,876 @@
+// Matrix products in 16-bit types with fp32 accumulation on tcgen05 (kind::f16): the dense
+// product with bias, activation and residual in its epilogue, the same product grouped by
+// expert over ragged row ranges, and their two gradients.
+//
+// Every product is written as out[j][i] = sum_c A[i][c] B[j][c], with i on the MMA's M (the
+// TMEM lanes) and j on its N (the columns):
+//   forward       i = output feature, j = token row, c = input feature   A = W,   B = x
+//   input grad    i = input feature,  j = token row, c = output feature  A = W^T, B = dz
+//   weight grad   i = input feature,  j = output feature, c = token row  A = x^T, B = dz^T
+// The transposed operands are read as they lie in memory, as MN-major operands.  Token rows on
+// N rather than M: a ragged expert's last tile then takes an MMA as narrow as its rows (in
+// steps of 16), where a tile on M would always pay 128 rows, and a decode step's few tokens
+// take an N of 16 under a weight tile of 128 rows that streams through once.  Features on the
+// lanes: a warp's 32 lanes store 32 consecutive values of one output row, so any row can be
+// left out and no shared-memory transpose is needed.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "linear_ptx.cuh"
+#include "moe_linear.cuh"
+
+namespace moe {
+namespace {
+
+constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s: a stuck pipeline, not a slow one
+constexpr int kBK = 64;                       // contraction values per stage (a 128-byte row)
+
+struct LinParams {
+  int32_t rows, E, bf16, fn;
+  int32_t I;             // extent of i (columns of out)
+  int32_t J;             // extent of j (kWeightGrad: N; else the expert's rows)
+  int32_t C;             // extent of c (kWeightGrad: the expert's rows)
+  int32_t a_rows;        // kForward: rows of W per expert
+  int32_t n_it;          // tiles along i
+  int32_t nw_max;        // widest tile along j
+  int32_t n_jt;          // kWeightGrad: tiles along j
+  int32_t splits;        // CTAs of a cluster that share one tile's contraction
+  float limit;
+  const int32_t* offsets;
+  uint16_t* out;
+  int64_t ld_out;
+  int64_t out_expert;    // kWeightGrad: elements of out per expert
+  const float* bias;
+  const uint16_t* residual;
+  int64_t ld_res;
+  uint16_t* z;
+  int32_t* status;
+  int32_t inject_timeout;
+  const uint16_t* out_end;   // ends of out and z (bounds-checking builds)
+  const uint16_t* z_end;
+};
+
+// One tile of the output: rows j0 .. j0 + nj - 1 (token rows of the buffer, or rows of dW) and
+// columns i0 .. of expert e; the MMA's N is nw >= nj.
+struct LinTile {
+  int32_t e, i0, j0, nj, nw;
+  int32_t c0, clen;      // contraction range (kWeightGrad: token rows c0 .. c0 + clen - 1)
+  int32_t ok;
+};
+
+// ------------------------------------------------------------------------------ conversions
+__device__ __forceinline__ uint16_t to16(float v, bool bf) {
+  return bf ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+}
+__device__ __forceinline__ float from16(uint16_t v, bool bf) {
+  return bf ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+}
+
+// ------------------------------------------------------------------------------ activations
+// In fp32 with the hardware exponential: its relative error (a few 2^-23) and that of the
+// approximate divide are far below the 16-bit rounding that follows.
+// (1 + tanh v) / 2 = 1 / (1 + exp(-2 v)) and (1 + erf v) / 2 = erfc(-v) / 2 keep their relative
+// accuracy where the left sides cancel.
+__device__ __forceinline__ float gelu_arg(float z) { return 0.79788456f * z * (1.f + 0.044715f * z * z); }
+
+template <int FN>
+__device__ __forceinline__ float act_fn(float z) {
+  if (FN == MOE_FN_RELU) return z < 0.f ? 0.f : z;   // (NaN stays NaN)
+  if (FN == MOE_FN_SILU) return __fdividef(z, 1.f + __expf(-z));
+  if (FN == MOE_FN_GELU) return 0.5f * z * erfcf(-0.70710678f * z);
+  if (FN == MOE_FN_GELU_TANH) return __fdividef(z, 1.f + __expf(-2.f * gelu_arg(z)));
+  return z;
+}
+
+__device__ __forceinline__ float clamp_hi(float v, float L) { return v > L ? L : v; }    // NaN passes
+__device__ __forceinline__ float clamp_both(float v, float L) { return v > L ? L : (v < -L ? -L : v); }
+
+__device__ __forceinline__ float swiglu(float g, float u, float L) {
+  const float gc = clamp_hi(g, L);
+  return __fdividef(gc, 1.f + __expf(-gc)) * clamp_both(u, L);
+}
+
+// ------------------------------------------------------------------------------ ragged rows
+// Range [a, b) of expert e, forced into [0, rows] and into order; bad offsets raise *bad.
+__device__ __forceinline__ void expert_rows(const int32_t* off, int32_t rows, int e, int& a, int& b, bool& bad) {
+  const int ra = __ldg(off + e), rb = __ldg(off + e + 1);
+  a = min(max(ra, 0), rows);
+  b = min(max(rb, a), rows);
+  bad |= (a != ra) || (b != rb);
+}
+
+// Balanced tile width for cnt rows in tiles of at most nw_max, a multiple of `step`: the
+// number of tiles stays ceil(cnt / nw_max).
+__device__ __forceinline__ int tile_width(int cnt, int nt, int step) {
+  return nt > 0 ? ((cnt + nt - 1) / nt + step - 1) / step * step : step;
+}
+
+// Tile `item` of a forward or input-gradient product, found by one warp (E <= 256: 8 experts
+// per lane).  Tiles run expert by expert; within an expert, JFAST: its token tiles run
+// fastest (CTAs that start together then share a weight tile in L2), else its i tiles.
+template <bool JFAST>
+__device__ __forceinline__ LinTile find_row_tile(const LinParams& p, int64_t item, int step, int iw) {
+  const int lane = threadIdx.x & 31;
+  LinTile t;
+  t.ok = 0;
+  t.c0 = 0;
+  t.clen = p.C;
+  if (!p.offsets) {
+    const int nt = (p.rows + p.nw_max - 1) / p.nw_max, w = tile_width(p.rows, nt, step);
+    if (item < (int64_t)nt * p.n_it) {
+      const int jt = JFAST ? (int)(item % nt) : (int)(item / p.n_it);
+      const int it = JFAST ? (int)(item / nt) : (int)(item % p.n_it);
+      t.ok = 1;
+      t.e = 0;
+      t.i0 = it * iw;
+      t.j0 = jt * w;
+      t.nj = min(w, p.rows - t.j0);
+      t.nw = (t.nj + step - 1) / step * step;
+    }
+    return t;
+  }
+  int a[8], cnt[8], sum = 0;
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int e = 8 * lane + k;
+    a[k] = 0;
+    cnt[k] = 0;
+    if (e < p.E) {
+      int b;
+      expert_rows(p.offsets, p.rows, e, a[k], b, bad);
+      cnt[k] = b - a[k];
+    }
+    sum += (cnt[k] + p.nw_max - 1) / p.nw_max;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (__any_sync(0xffffffffu, bad) && item == 0 && lane == 0) set_status(p.status, MOE_ERR_INVALID_ARG);
+  const int64_t lo = (int64_t)(incl - sum) * p.n_it, hi = (int64_t)incl * p.n_it;
+  const unsigned who = __ballot_sync(0xffffffffu, item >= lo && item < hi);
+  if (!who) return t;
+  const int src = __ffs(who) - 1;
+  int fe = 0, fa = 0, fc = 0, floc = 0;
+  if (lane == src) {
+    int64_t base = lo;
+    bool found = false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t n = (int64_t)((cnt[k] + p.nw_max - 1) / p.nw_max) * p.n_it;
+      if (!found && item < base + n) {
+        found = true;
+        fe = 8 * lane + k;
+        fa = a[k];
+        fc = cnt[k];
+        floc = (int)(item - base);
+      }
+      base += n;
+    }
+  }
+  fe = __shfl_sync(0xffffffffu, fe, src);
+  fa = __shfl_sync(0xffffffffu, fa, src);
+  fc = __shfl_sync(0xffffffffu, fc, src);
+  floc = __shfl_sync(0xffffffffu, floc, src);
+  const int nt = (fc + p.nw_max - 1) / p.nw_max, w = tile_width(fc, nt, step);
+  const int jt = JFAST ? floc % nt : floc / p.n_it, it = JFAST ? floc / nt : floc % p.n_it;
+  t.ok = 1;
+  t.e = fe;
+  t.i0 = it * iw;
+  t.j0 = fa + jt * w;
+  t.nj = min(w, fc - jt * w);
+  t.nw = (t.nj + step - 1) / step * step;
+  return t;
+}
+
+// Tile `item` of a weight gradient: every expert has the same tiles, its own contraction range.
+__device__ __forceinline__ LinTile find_weight_tile(const LinParams& p, int64_t item, int step, int iw) {
+  LinTile t;
+  const int per_e = p.n_it * p.n_jt;
+  t.ok = item < (int64_t)per_e * p.E;
+  if (!t.ok) return t;
+  t.e = (int)(item / per_e);
+  const int loc = (int)(item - (int64_t)t.e * per_e);
+  const int w = tile_width(p.J, p.n_jt, step);
+  t.i0 = (loc % p.n_it) * iw;
+  t.j0 = (loc / p.n_it) * w;
+  t.nj = min(w, p.J - t.j0);
+  t.nw = (max(t.nj, 1) + step - 1) / step * step;
+  t.c0 = 0;
+  t.clen = p.rows;
+  if (p.offsets) {
+    int b;
+    bool bad = false;
+    expert_rows(p.offsets, p.rows, t.e, t.c0, b, bad);
+    t.clen = b - t.c0;
+    if (bad && loc == 0 && (threadIdx.x & 31) == 0) set_status(p.status, MOE_ERR_INVALID_ARG);
+  }
+  return t;
+}
+
+template <int MODE, bool JFAST>
+__device__ __forceinline__ LinTile find_tile(const LinParams& p, int64_t item, int step, int iw) {
+  if (MODE == kWeightGrad) return find_weight_tile(p, item, step, iw);
+  return find_row_tile<JFAST>(p, item, step, iw);
+}
+
+// Token rows c .. c + 63 of a weight gradient's contraction block as coordinates (d1, d2) of
+// the rank-3 view [rows][64][values] whose two row axes share one stride: row d1 + d2, and d1
+// outside [0, 64) reads zeros.  A block of n < 64 rows is loaded with 64 - n rows of zeros in
+// front (d1 starts at n - 64), so no row of another expert (its values may be infinite) enters
+// the sum; both operands shift alike, and the order of c does not matter.
+__device__ __forceinline__ int tail_shift(int n) { return n < kBK ? n - kBK : 0; }
+
+// ------------------------------------------------------------------------------ epilogue
+// One accumulator value (NA = 2: the gate's and the up's) to the outputs at (row, i).
+template <int FN>
+__device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t, const uint32_t (&va)[32],
+                                            const uint32_t (&vb)[32], int col0, int i, float bias_a, float bias_b) {
+  const bool bf = p.bf16 != 0;
+  if (i >= p.I) return;
+  const int n = min(32, t.nj - col0);   // valid columns (may be <= 0)
+  uint16_t* out = p.out + t.e * p.out_expert + i;
+  uint16_t* z = p.z ? p.z + i : nullptr;
+  const int64_t ldz = (FN == MOE_FN_SWIGLU ? 2 : 1) * (int64_t)p.I;
+  uint16_t res[32];
+  if (p.residual) {
+    const uint16_t* r = p.residual + i;
+#pragma unroll
+    for (int c = 0; c < 32; ++c)
+      if (c < n) res[c] = r[(int64_t)(t.j0 + col0 + c) * p.ld_res];   // (y may be this buffer: no read-only path)
+  }
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    if (c >= n) break;
+    const int64_t row = t.j0 + col0 + c;
+    const float a = __uint_as_float(va[c]) + bias_a;
+    float y;
+    if (FN == MOE_FN_SWIGLU) {
+      const float u = __uint_as_float(vb[c]) + bias_b;
+      if (z) {
+        uint16_t* q = z + row * ldz;
+        if (in_bounds(q + p.I, p.z, p.z_end, p.status)) {
+          q[0] = to16(a, bf);
+          q[p.I] = to16(u, bf);
+        }
+      }
+      y = swiglu(a, u, p.limit);
+    } else {
+      if (z) {
+        uint16_t* q = z + row * ldz;
+        if (in_bounds(q, p.z, p.z_end, p.status)) *q = to16(a, bf);
+      }
+      y = act_fn<FN>(a);
+    }
+    if (p.residual) y += from16(res[c], bf);
+    uint16_t* q = out + row * p.ld_out;
+    if (in_bounds(q, p.out, p.out_end, p.status)) *q = to16(y, bf);
+  }
+}
+
+template <int MODE, int NA>
+__device__ __forceinline__ void finish(const LinParams& p, const LinTile& t, const uint32_t (&va)[32],
+                                       const uint32_t (&vb)[32], int col0, int i, float bias_a, float bias_b) {
+  if (NA == 2) return finish_cols<MOE_FN_SWIGLU>(p, t, va, vb, col0, i, bias_a, bias_b);
+  if (MODE == kForward) {
+    switch (p.fn) {
+      case MOE_FN_RELU: return finish_cols<MOE_FN_RELU>(p, t, va, vb, col0, i, bias_a, bias_b);
+      case MOE_FN_GELU: return finish_cols<MOE_FN_GELU>(p, t, va, vb, col0, i, bias_a, bias_b);
+      case MOE_FN_GELU_TANH: return finish_cols<MOE_FN_GELU_TANH>(p, t, va, vb, col0, i, bias_a, bias_b);
+      case MOE_FN_SILU: return finish_cols<MOE_FN_SILU>(p, t, va, vb, col0, i, bias_a, bias_b);
+    }
+  }
+  finish_cols<MOE_FN_NONE>(p, t, va, vb, col0, i, bias_a, bias_b);
+}
+
+// ------------------------------------------------------------------------------ split kernel
+// One CTA (or a cluster of `splits` CTAs that share a tile's contraction) per output tile of
+// 128 i x at most NB j (NA = 2: 128 gate and the matching 128 up features).
+template <int MODE, int NA, int NB>
+struct SplitCfg {
+  static constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeightGrad;
+  static constexpr int A_PANEL = 128 * 128;             // 128 i x 64 c of 2 bytes
+  static constexpr int B_BOX = NB < 64 ? NB : 64;       // j per copy of B
+  static constexpr int B_BYTES = NB * 128;
+  static constexpr int STAGE = NA * A_PANEL + B_BYTES;
+  static constexpr int CPS = (NA == 2 && NB == 128) ? 1 : 2;   // CTAs per SM
+  static constexpr int S = ((CPS == 1 ? 200 : 108) * 1024) / STAGE > 6 ? 6 : ((CPS == 1 ? 200 : 108) * 1024) / STAGE;
+  static constexpr int COLS = NA * NB;
+  static constexpr int TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
+  static constexpr int RED_BYTES = COLS * 128 * 4;      // fp32 partial tile (reuses the stages)
+  static constexpr int BAR_BYTES = 8 * (2 * S + 2) + 64;
+  static constexpr int SMEM = S * STAGE + BAR_BYTES + 1024 /* align slack */;
+  static constexpr int THREADS = 32 * 6;                // producer, MMA, four epilogue warps
+  static_assert(RED_BYTES <= S * STAGE, "the partial tile fits the stages");
+  static_assert((SMEM + 1024) * CPS <= 228 * 1024, "shared memory of the co-resident CTAs");
+  static_assert(COLS * CPS <= 512, "TMEM of the co-resident CTAs");
+  static_assert(NB % 32 == 0 && NB <= 256 && (!B_MN || NB % 64 == 0), "tile width");
+};
+
+template <int MODE, int NA, int NB>
+__global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE, NA, NB>::CPS)
+    lin_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const LinParams p) {
+  using C = SplitCfg<MODE, NA, NB>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::S * C::STAGE);
+  uint64_t* sfree = full + C::S;
+  uint64_t* accf = sfree + C::S;
+  uint64_t* drain = accf + 1;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  LinTile* s_tile = reinterpret_cast<LinTile*>(s_tmem + 2);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int S = p.splits;
+  const int rank = S > 1 ? (int)ptx::cluster_ctarank() : 0;
+  const int64_t item = blockIdx.x / S;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < C::S; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&sfree[s], 1);
+    }
+    ptx::mbar_init(accf, 1);
+    ptx::mbar_init(drain, 1);
+    *s_abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&tm_a);
+    ptx::prefetch_tensormap(&tm_b);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(s_tmem, C::TMEM_COLS);
+    ptx::tmem_relinquish();
+    ptx::tc_fence_before();
+  }
+  if (warp == 2) {
+    const LinTile t = find_tile<MODE, true>(p, item, 16, 128);
+    if (lane == 0) *s_tile = t;
+  }
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const LinTile t = *s_tile;
+  const int kb_all = t.ok ? (t.clen + kBK - 1) / kBK : 0;
+  const int kb0 = (int)((int64_t)rank * kb_all / S), kb1 = (int)((int64_t)(rank + 1) * kb_all / S);
+  const int nbox = (t.nw + C::B_BOX - 1) / C::B_BOX;   // copies of B per stage
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer
+    int g = 0;
+    bool withheld = false;
+    for (int kb = kb0; kb < kb1; ++kb, ++g) {
+      const int s = g % C::S;
+      bool ok = true;
+      if (g >= C::S) ok = ptx::mbar_wait_bounded(&sfree[s], (uint32_t)(g / C::S - 1) & 1, s_abort, kWaitNs);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      if (p.inject_timeout && blockIdx.x == 0 && g == 0) {
+        withheld = true;   // test hook: this stage never fills
+        continue;
+      }
+      if (ptx::elect_one()) {
+        uint8_t* a = smem + s * C::STAGE;
+        uint8_t* b = a + NA * C::A_PANEL;
+        ptx::mbar_arrive_expect_tx(&full[s], NA * C::A_PANEL + nbox * C::B_BOX * 128);
+        const int c = kb * kBK;
+        if (MODE == kForward) {
+#pragma unroll
+          for (int h = 0; h < NA; ++h)
+            ptx::tma_load_2d(a + h * C::A_PANEL, &tm_a, c, t.e * p.a_rows + h * p.I + t.i0, &full[s]);
+        } else if (MODE == kInputGrad) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) ptx::tma_load_3d(a + h * 8192, &tm_a, t.i0 + 64 * h, c, t.e, &full[s]);
+        }
+        if (MODE == kWeightGrad) {
+          const int d1 = tail_shift(t.clen - c), d2 = t.c0 + c;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) ptx::tma_load_3d(a + h * 8192, &tm_a, t.i0 + 64 * h, d1, d2, &full[s]);
+          for (int h = 0; h < nbox; ++h) ptx::tma_load_3d(b + h * 8192, &tm_b, t.j0 + 64 * h, d1, d2, &full[s]);
+        } else {
+          for (int h = 0; h < nbox; ++h)
+            ptx::tma_load_2d(b + h * C::B_BOX * 128, &tm_b, c, t.j0 + C::B_BOX * h, &full[s]);
+        }
+      }
+      __syncwarp();
+    }
+    // no copies in flight when the CTA exits: wait (bounded) for the last fill of every slot
+    volatile int local_abort = 0;
+    for (int q = (g > C::S ? g - C::S : 0); q < g; ++q) {
+      if (withheld && q == 0) continue;
+      ptx::mbar_wait_bounded(&full[q % C::S], (uint32_t)(q / C::S) & 1, &local_abort, kWaitNs);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer
+    const uint32_t idesc = ptx::idesc_f16(p.bf16 != 0, 128, t.nw, C::A_MN, C::B_MN);
+    // a 16-wide step of c: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
+    constexpr uint64_t kStepA = C::A_MN ? 2048 >> 4 : 32 >> 4, kStepB = C::B_MN ? 2048 >> 4 : 32 >> 4;
+    int g = 0;
+    bool stop = false;
+    for (int kb = kb0; kb < kb1; ++kb, ++g) {
+      const int s = g % C::S;
+      if (!__all_sync(0xffffffffu,
+                      ptx::mbar_wait_bounded(&full[s], (uint32_t)(g / C::S) & 1, s_abort, kWaitNs))) {
+        stop = true;
+        break;
+      }
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        const uint8_t* a = smem + s * C::STAGE;
+        const uint8_t* b = a + NA * C::A_PANEL;
+        const uint64_t da = C::A_MN ? ptx::smem_desc_mn_sw128(a) : ptx::smem_desc_k_sw128(a);
+        const uint64_t db = C::B_MN ? ptx::smem_desc_mn_sw128(b) : ptx::smem_desc_k_sw128(b);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+          for (int h = 0; h < NA; ++h)
+            ptx::mma_f16_ss(tmem + h * NB, da + h * (C::A_PANEL >> 4) + k * kStepA, db + k * kStepB, idesc,
+                            (g | k) != 0);
+        }
+        ptx::tc_commit(&sfree[s]);
+      }
+      __syncwarp();
+    }
+    if (ptx::elect_one()) {
+      if (!stop) ptx::tc_commit(accf);
+      ptx::tc_commit(drain);
+    }
+    __syncwarp();
+    volatile int local_abort = 0;
+    ptx::mbar_wait_bounded(drain, 0, &local_abort, kWaitNs);
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- epilogue warps
+    const int q = warp & 3, row = 32 * q + lane, i = t.i0 + row;
+    const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
+    const bool have = kb1 > kb0;
+    const bool ready = ptx::mbar_wait_bounded(accf, 0, s_abort, kWaitNs);
+    if (!ptx::bar_or<1, 128>(!ready) && t.ok) {
+      ptx::tc_fence_after();
+      float bias_a = 0.f, bias_b = 0.f;
+      if (MODE == kForward && p.bias && i < p.I) {
+        bias_a = __ldg(p.bias + (int64_t)t.e * p.a_rows + i);
+        if (NA == 2) bias_b = __ldg(p.bias + (int64_t)t.e * p.a_rows + p.I + i);
+      }
+      float* red = reinterpret_cast<float*>(smem);
+      for (int c0 = 0; c0 < t.nw; c0 += 32) {
+        uint32_t va[32], vb[32];
+        ptx::tmem_ld32(acc + c0, va);
+        if (NA == 2) ptx::tmem_ld32(acc + NB + c0, vb);
+        ptx::tmem_wait_ld();
+        if (!have) {   // no contraction block here: the accumulator was never written
+#pragma unroll
+          for (int c = 0; c < 32; ++c) va[c] = vb[c] = 0u;
+        }
+        if (S == 1) {
+          finish<MODE, NA>(p, t, va, vb, c0, i, bias_a, bias_b);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            red[(c0 + c) * 128 + row] = __uint_as_float(va[c]);
+            if (NA == 2) red[(NB + c0 + c) * 128 + row] = __uint_as_float(vb[c]);
+          }
+        }
+      }
+    }
+  }
+
+  __syncthreads();
+  if (*s_abort && threadIdx.x == 0) set_status(p.status, MOE_ERR_TIMEOUT);
+  if (S > 1) {
+    // The cluster's partial tiles meet over distributed shared memory: CTA r adds and finishes
+    // its share of the columns, in rank order, so that the sum does not depend on timing.
+    ptx::cluster_sync();
+    if (warp >= 2 && t.ok) {
+      const int q = warp & 3, row = 32 * q + lane, i = t.i0 + row;
+      float bias_a = 0.f, bias_b = 0.f;
+      if (MODE == kForward && p.bias && i < p.I) {
+        bias_a = __ldg(p.bias + (int64_t)t.e * p.a_rows + i);
+        if (NA == 2) bias_b = __ldg(p.bias + (int64_t)t.e * p.a_rows + p.I + i);
+      }
+      const int per = (t.nw + S - 1) / S;   // columns per CTA
+      const int c1 = min((rank + 1) * per, t.nj);
+      for (int c0 = rank * per; c0 < c1; c0 += 32) {
+        uint32_t va[32], vb[32];
+        LinTile tt = t;
+        tt.nj = c1;
+        const int n = min(32, c1 - c0);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float sa = 0.f, sb = 0.f;
+          if (c < n) {
+            for (int r = 0; r < S; ++r) {
+              sa += ptx::ld_cluster_f32(ptx::mapa_shared(smem + ((c0 + c) * 128 + row) * 4, r));
+              if (NA == 2) sb += ptx::ld_cluster_f32(ptx::mapa_shared(smem + ((NB + c0 + c) * 128 + row) * 4, r));
+            }
+          }
+          va[c] = __float_as_uint(sa);
+          vb[c] = __float_as_uint(sb);
+        }
+        finish<MODE, NA>(p, tt, va, vb, c0, i, bias_a, bias_b);
+      }
+    }
+    ptx::cluster_sync();   // no CTA leaves while a peer reads its partial tile
+  }
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ------------------------------------------------------------------------------ host side
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(f);
+  });
+  return fn;
+}
+
+// Map of 16-bit values, 128-byte swizzle, boxes of 64 values x box1 x 1; strides in values.
+bool map16(CUtensorMap* m, bool bf16, const void* base, int rank, uint64_t d0, uint64_t d1, uint64_t s1, uint64_t d2,
+           uint64_t s2, uint32_t box1) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {2 * s1, 2 * s2};
+  const cuuint32_t box[3] = {64, box1, 1}, es[3] = {1, 1, 1};
+  return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
+            const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The operand maps of a product: a_box / b_box rows per copy of the K-major ones.
+bool operand_maps(const LinArgs& a, uint32_t a_box, uint32_t b_box, CUtensorMap* ma, CUtensorMap* mb) {
+  const bool bf = a.bf16 != 0;
+  const uint64_t K = a.K, N = a.N, E = a.E, rows = a.rows;
+  switch (a.mode) {
+    case kForward:   // W [E * N][K], x [rows][K]
+      return map16(ma, bf, a.other, 2, K, E * N, K, 1, 0, a_box) &&
+             map16(mb, bf, a.tok, 2, K, rows, a.ld_tok, 1, 0, b_box);
+    case kInputGrad: // W [E][N][K] (rows past an expert's N read zeros), dz [rows][N]
+      return map16(ma, bf, a.other, 3, K, N, K, E, N * K, 64) &&
+             map16(mb, bf, a.tok, 2, N, rows, a.ld_tok, 1, 0, b_box);
+    default:         // x, dz as [rows][64][values]: see tail_shift
+      return map16(ma, bf, a.other, 3, K, 64, a.ld_other, rows, a.ld_other, 64) &&
+             map16(mb, bf, a.tok, 3, N, 64, a.ld_tok, rows, a.ld_tok, 64);
+  }
+}
+
+// Kernels' dynamic shared memory limit, set once per device.
+template <class K>
+bool allow_smem(K kern, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+  if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return true;
+}
+
+LinParams params_of(const LinArgs& a, int iw) {
+  LinParams p = {};
+  const int No = a.fn == MOE_FN_SWIGLU ? a.N / 2 : a.N;
+  p.rows = a.rows;
+  p.E = a.E;
+  p.bf16 = a.bf16;
+  p.fn = a.fn;
+  p.limit = a.limit;
+  p.I = a.mode == kForward ? No : a.K;
+  p.J = a.N;
+  p.C = a.mode == kForward ? a.K : a.N;
+  p.a_rows = a.N;
+  p.n_it = (p.I + iw - 1) / iw;
+  p.offsets = a.offsets;
+  p.out = static_cast<uint16_t*>(a.out);
+  p.ld_out = a.mode == kWeightGrad ? a.K : a.ld_out;
+  p.out_expert = a.mode == kWeightGrad ? (int64_t)a.N * a.K : 0;
+  p.bias = a.bias;
+  p.residual = static_cast<const uint16_t*>(a.residual);
+  p.ld_res = a.ld_res;
+  p.z = static_cast<uint16_t*>(a.z);
+  p.status = a.status;
+  p.inject_timeout = a.inject_timeout;
+  const int64_t out_n = a.mode == kWeightGrad ? (int64_t)a.E * a.N * a.K : (int64_t)(a.rows - 1) * a.ld_out + p.I;
+  p.out_end = p.out + out_n;
+  p.z_end = p.z ? p.z + (int64_t)a.rows * a.N : nullptr;
+  return p;
+}
+
+// Most token tiles of at most nw rows that `rows` rows of E experts can make.
+int64_t row_tiles_bound(const LinArgs& a, int nw) {
+  if (!a.offsets) return (a.rows + nw - 1) / nw;
+  const int64_t used = std::min(a.E, a.rows);
+  return (a.rows - used) / nw + used;
+}
+
+template <int MODE, int NA, int NB>
+int launch_split(const LinArgs& a) {
+  using C = SplitCfg<MODE, NA, NB>;
+  CUtensorMap ma, mb;
+  if (!operand_maps(a, 128, C::B_BOX, &ma, &mb)) return -1;
+  LinParams p = params_of(a, 128);
+  p.nw_max = NB;
+  p.n_jt = (a.N + NB - 1) / NB;
+  const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, NB)) * p.n_it;
+  // Fewer tiles than the GPU holds CTAs: a cluster shares each tile's contraction, every CTA
+  // keeping at least two 64-wide blocks of it.
+  const int64_t blocks = MODE == kWeightGrad ? (a.rows / (a.offsets ? a.E : 1) + kBK - 1) / kBK : (p.C + kBK - 1) / kBK;
+  int64_t s = std::min<int64_t>((int64_t)multiprocessors() * C::CPS / tiles, blocks / 2);
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, 8));
+  auto kern = lin_split_kernel<MODE, NA, NB>;
+  static std::atomic<uint64_t> done{0};
+  if (!allow_smem(kern, C::SMEM, done)) return -1;
+  const int64_t grid = tiles * p.splits;
+  if (grid > 0x7fffffff) return -1;
+  const dim3 g((unsigned)grid), b(C::THREADS);
+  const cudaError_t err = p.splits == 1
+      ? launch_kernel(kern, g, b, C::SMEM, a.stream, false, ma, mb, p)
+      : launch_kernel_cluster(kern, g, b, C::SMEM, a.stream, false, (unsigned)p.splits, ma, mb, p);
+  return err == cudaSuccess ? 1 : -1;
+}
+
+}  // namespace
+
+int launch_linear(const LinArgs& a) {
+  const bool narrow = a.rows <= 32 * (a.offsets ? a.E : 1);   // few rows an expert: the weights' stream is the work
+  switch (a.mode) {
+    case kForward:
+      if (a.fn == MOE_FN_SWIGLU) return narrow ? launch_split<kForward, 2, 32>(a) : launch_split<kForward, 2, 128>(a);
+      return narrow ? launch_split<kForward, 1, 32>(a) : launch_split<kForward, 1, 128>(a);
+    case kInputGrad:
+      return narrow ? launch_split<kInputGrad, 1, 32>(a) : launch_split<kInputGrad, 1, 128>(a);
+    default:
+      return launch_split<kWeightGrad, 1, 128>(a);
+  }
+}
+
+// ------------------------------------------------------------------------------ activation gradient
+// dz = dy f'(z) and the column sums db of dz, in one pass over dy and z.  A block takes a chunk
+// of kChunk rows of one expert and 256 columns, 8 per lane; its 8 warps take rows in turn and
+// add their column sums in a fixed order into one row of `partial`, which sum_chunks_kernel
+// adds up per expert.  The sums take dz before its rounding to 16 bits.
+namespace {
+constexpr int kChunk = 64;
+
+struct ActGradParams {
+  int32_t rows, N, No, E, bf16, fn, chunks;
+  float limit;
+  const int32_t* offsets;
+  const uint16_t* dy;
+  int64_t ld_dy;
+  const uint16_t* z;
+  uint16_t* dz;
+  float* partial;
+  float* db;
+  int32_t* status;
+};
+
+template <int FN>
+__device__ __forceinline__ float act_grad(float z, float dy) {
+  if (FN == MOE_FN_RELU) return z > 0.f ? dy : 0.f;
+  if (FN == MOE_FN_SILU) {
+    const float s = __fdividef(1.f, 1.f + __expf(-z));
+    return dy * s * (1.f + z * (1.f - s));
+  }
+  if (FN == MOE_FN_GELU)
+    return dy * (0.5f * erfcf(-0.70710678f * z) + z * __expf(-0.5f * z * z) * 0.39894228f);
+  if (FN == MOE_FN_GELU_TANH) {   // s = (1 + tanh v) / 2, (1 - tanh^2 v) / 2 = 2 s (1 - s)
+    const float s = __fdividef(1.f, 1.f + __expf(-2.f * gelu_arg(z)));
+    return dy * (s + 2.f * z * s * (1.f - s) * 0.79788456f * (1.f + 0.134145f * z * z));
+  }
+  return dy;
+}
+
+// Chunk q of the ragged rows -> (expert, first row, rows); one warp, as find_row_tile.
+__device__ __forceinline__ bool find_chunk(const ActGradParams& p, int q, int& e, int& r0, int& n) {
+  LinParams lp;
+  lp.rows = p.rows;
+  lp.E = p.E;
+  lp.offsets = p.offsets;
+  lp.n_it = 1;
+  lp.nw_max = kChunk;
+  lp.C = 0;
+  lp.status = p.status;
+  const LinTile t = find_row_tile<true>(lp, q, kChunk, 0);
+  e = t.e;
+  r0 = t.j0;
+  n = t.nj;
+  return t.ok != 0;
+}
+
+template <int FN>
+__global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
+  __shared__ int s_t[4];
+  __shared__ float s_sum[8][256];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    int e = 0, r0 = 0, n = 0;
+    const bool ok = find_chunk(p, blockIdx.x, e, r0, n);
+    if (lane == 0) {
+      s_t[0] = ok;
+      s_t[1] = r0;
+      s_t[2] = n;
+    }
+  }
+  __syncthreads();
+  if (!s_t[0]) return;
+  const int r0 = s_t[1], n = s_t[2];
+  const bool bf = p.bf16 != 0;
+  const int col = blockIdx.y * 256 + 8 * lane;      // of [0, N): SwiGLU gate columns, then up columns
+  const bool in = col < p.N;                        // (N is a multiple of 8)
+  float sum[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+  if (in) {
+    for (int r = r0 + warp; r < r0 + n; r += 8) {
+      float o[8];
+      uint4 zv, dv;
+      if (FN == MOE_FN_SWIGLU) {
+        const int c = col < p.No ? col : col - p.No;
+        const uint4 gv = __ldg(reinterpret_cast<const uint4*>(p.z + (int64_t)r * p.N + c));
+        const uint4 uv = __ldg(reinterpret_cast<const uint4*>(p.z + (int64_t)r * p.N + p.No + c));
+        dv = __ldg(reinterpret_cast<const uint4*>(p.dy + (int64_t)r * p.ld_dy + c));
+        const uint16_t* g16 = reinterpret_cast<const uint16_t*>(&gv);
+        const uint16_t* u16 = reinterpret_cast<const uint16_t*>(&uv);
+        const uint16_t* d16 = reinterpret_cast<const uint16_t*>(&dv);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float g0 = from16(g16[k], bf), u0 = from16(u16[k], bf), d = from16(d16[k], bf);
+          const float g = clamp_hi(g0, p.limit), u = clamp_both(u0, p.limit);
+          const float s = __fdividef(1.f, 1.f + __expf(-g));
+          if (col < p.No) o[k] = g0 > p.limit ? 0.f : d * u * s * (1.f + g * (1.f - s));
+          else o[k] = fabsf(u0) <= p.limit ? d * g * s : 0.f;
+        }
+      } else {
+        dv = __ldg(reinterpret_cast<const uint4*>(p.dy + (int64_t)r * p.ld_dy + col));
+        if (FN != MOE_FN_NONE) zv = __ldg(reinterpret_cast<const uint4*>(p.z + (int64_t)r * p.N + col));
+        const uint16_t* d16 = reinterpret_cast<const uint16_t*>(&dv);
+        const uint16_t* z16 = reinterpret_cast<const uint16_t*>(&zv);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          o[k] = act_grad<FN>(FN != MOE_FN_NONE ? from16(z16[k], bf) : 0.f, from16(d16[k], bf));
+      }
+      if (FN != MOE_FN_NONE) {
+        uint4 ov;
+        uint16_t* o16 = reinterpret_cast<uint16_t*>(&ov);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o16[k] = to16(o[k], bf);
+        *reinterpret_cast<uint4*>(p.dz + (int64_t)r * p.N + col) = ov;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] += o[k];
+    }
+  }
+  if (!p.partial) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) s_sum[warp][8 * lane + k] = sum[k];
+  __syncthreads();
+  const int c = blockIdx.y * 256 + threadIdx.x;
+  if (c < p.N) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += s_sum[w][threadIdx.x];
+    p.partial[(int64_t)blockIdx.x * p.N + c] = v;
+  }
+}
+
+// db[e][n] = the sum of expert e's chunks (none: 0), in order: 8 warps take every eighth chunk
+// and their sums are added in warp order.
+__global__ void __launch_bounds__(256) sum_chunks_kernel(const ActGradParams p) {
+  __shared__ float s_sum[8][32];
+  __shared__ int s_first;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.y;
+  int a = 0, b = p.rows;
+  bool bad = false;
+  if (p.offsets) {
+    expert_rows(p.offsets, p.rows, e, a, b, bad);
+    if (warp == 0) {   // first chunk of expert e: the chunks of the experts before it
+      int n = 0;
+      for (int q = lane; q < e; q += 32) {
+        int qa, qb;
+        expert_rows(p.offsets, p.rows, q, qa, qb, bad);
+        n += (qb - qa + kChunk - 1) / kChunk;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (lane == 0) s_first = n;
+    }
+  } else if (threadIdx.x == 0) {
+    s_first = 0;
+  }
+  __syncthreads();
+  // (offsets out of order could count past the rows of `partial`)
+  const int first = s_first, n = min((b - a + kChunk - 1) / kChunk, p.chunks - first), c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < p.N)
+    for (int q = warp; q < n; q += 8) v += p.partial[(int64_t)(first + q) * p.N + c];
+  s_sum[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < p.N) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) t += s_sum[w][lane];
+    p.db[(int64_t)e * p.N + c] = t;
+  }
+}
+}  // namespace
+
+int64_t act_grad_chunks(int32_t rows, int32_t E) {
+  const int64_t used = std::min(E, rows);
+  return used + (rows - used) / kChunk;   // the most that ragged counts can make
+}
+
+int launch_act_grad(const ActGradArgs& a) {
+  ActGradParams p = {};
+  p.rows = a.rows;
+  p.N = a.N;
+  p.No = a.fn == MOE_FN_SWIGLU ? a.N / 2 : a.N;
+  p.E = a.E;
+  p.bf16 = a.bf16;
+  p.fn = a.fn;
+  p.limit = a.limit;
+  p.offsets = a.offsets;
+  p.dy = static_cast<const uint16_t*>(a.dy);
+  p.ld_dy = a.ld_dy;
+  p.z = static_cast<const uint16_t*>(a.z);
+  p.dz = static_cast<uint16_t*>(a.dz);
+  p.partial = a.db ? a.partial : nullptr;
+  p.db = a.db;
+  p.status = a.status;
+  p.chunks = (int)act_grad_chunks(a.rows, a.offsets ? a.E : 1);
+  const dim3 grid((unsigned)p.chunks, (unsigned)((a.N + 255) / 256));
+  auto kern = act_grad_kernel<MOE_FN_NONE>;
+  switch (a.fn) {
+    case MOE_FN_RELU: kern = act_grad_kernel<MOE_FN_RELU>; break;
+    case MOE_FN_GELU: kern = act_grad_kernel<MOE_FN_GELU>; break;
+    case MOE_FN_GELU_TANH: kern = act_grad_kernel<MOE_FN_GELU_TANH>; break;
+    case MOE_FN_SILU: kern = act_grad_kernel<MOE_FN_SILU>; break;
+    case MOE_FN_SWIGLU: kern = act_grad_kernel<MOE_FN_SWIGLU>; break;
+  }
+  if (launch_kernel(kern, grid, dim3(256), 0, a.stream, false, p) != cudaSuccess) return -1;
+  if (!a.db) return 1;
+  if (launch_kernel(sum_chunks_kernel, dim3((unsigned)((a.N + 31) / 32), (unsigned)a.E), dim3(256), 0, a.stream, false,
+                    p) != cudaSuccess)
+    return -1;
+  return 2;
+}
+
+}  // namespace moe
