@@ -220,6 +220,86 @@ __device__ __forceinline__ LinTile find_tile(const LinParams& p, int64_t item, i
   return find_row_tile<JFAST>(p, item, step, iw);
 }
 
+// The experts' row ranges and tiles, kept in shared memory by kernels that take many tiles.
+struct RowTable {
+  int64_t items;
+  int32_t start[256], cnt[256];
+  int32_t base[257];         // first tile (along j) of each expert
+};
+
+// Built by one warp (8 experts per lane).
+template <int MODE>
+__device__ __forceinline__ void build_table(const LinParams& p, RowTable* tab) {
+  const int lane = threadIdx.x & 31;
+  int cnt[8], sum = 0;
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int e = 8 * lane + k;
+    int a = 0;
+    cnt[k] = 0;
+    if (e < p.E) {
+      int b = p.rows;
+      if (p.offsets) expert_rows(p.offsets, p.rows, e, a, b, bad);
+      cnt[k] = b - a;
+    }
+    tab->start[e] = a;
+    tab->cnt[e] = cnt[k];
+    sum += MODE == kWeightGrad ? (e < p.E ? p.n_jt : 0) : (cnt[k] + p.nw_max - 1) / p.nw_max;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int at = incl - sum;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int e = 8 * lane + k;
+    tab->base[e] = at;
+    at += MODE == kWeightGrad ? (e < p.E ? p.n_jt : 0) : (cnt[k] + p.nw_max - 1) / p.nw_max;
+  }
+  if (lane == 31) {
+    tab->base[256] = incl;
+    tab->items = (int64_t)incl * p.n_it;
+  }
+  if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) set_status(p.status, MOE_ERR_INVALID_ARG);
+}
+
+// Tile `item` (< items) by the whole warp: expert by expert, tiles along i fastest.
+template <int MODE>
+__device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable* tab, int64_t item, int step, int iw) {
+  const int lane = threadIdx.x & 31;
+  const int q = (int)(item / p.n_it);
+  LinTile t;
+  t.ok = 1;
+  t.i0 = (int)(item - (int64_t)q * p.n_it) * iw;
+  t.e = 0;
+  if (p.E > 1) {   // the lane, then the expert of its eight, whose tiles hold q
+    const unsigned m = __ballot_sync(0xffffffffu, tab->base[8 * lane] <= q && q < tab->base[8 * lane + 8]);
+    const int e = 8 * (__ffs(m) - 1) + (lane & 7);
+    const unsigned m8 = __ballot_sync(0xffffffffu, tab->base[e] <= q && q < tab->base[e + 1]);
+    t.e = 8 * (__ffs(m) - 1) + __ffs(m8) - 1;
+  }
+  const int jt = q - tab->base[t.e], cnt = tab->cnt[t.e], start = tab->start[t.e];
+  if (MODE == kWeightGrad) {
+    const int w = tile_width(p.J, p.n_jt, step);
+    t.j0 = jt * w;
+    t.nj = min(w, p.J - t.j0);
+    t.c0 = start;
+    t.clen = cnt;
+  } else {
+    const int w = tile_width(cnt, (cnt + p.nw_max - 1) / p.nw_max, step);
+    t.j0 = start + jt * w;
+    t.nj = min(w, cnt - jt * w);
+    t.c0 = 0;
+    t.clen = p.C;
+  }
+  t.nw = (max(t.nj, 1) + step - 1) / step * step;
+  return t;
+}
+
 // Token rows c .. c + 63 of a weight gradient's contraction block as coordinates (d1, d2) of
 // the rank-3 view [rows][64][values] whose two row axes share one stride: row d1 + d2, and d1
 // outside [0, 64) reads zeros.  A block of n < 64 rows is loaded with 64 - n rows of zeros in
@@ -525,6 +605,227 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE
   }
 }
 
+// ------------------------------------------------------------------------------ pair kernel
+// Large products: persistent CTA pairs (cta_group::2, one MMA of M = 256 over two SMs), tiles of
+// 256 i x at most 256 j (NA = 2: 256 gate and the matching 256 up features x at most 128 j).
+// Each CTA holds its 128 rows of A (and of the second accumulator's A) and half of B's rows, so a
+// pair moves half the bytes into shared memory per multiply-add that two single CTAs would.  The
+// accumulator is double-buffered in TMEM: the epilogue of a tile runs under the next tile's MMAs.
+template <int MODE, int NA>
+struct PairCfg {
+  static constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeightGrad;
+  static constexpr int NB = 256 / NA;                   // widest tile along j
+  static constexpr int A_PANEL = 128 * 128;
+  static constexpr int B_BYTES = NB / 2 * 128;          // this CTA's half of B
+  static constexpr int STAGE = NA * A_PANEL + B_BYTES;
+  static constexpr int S = 200 * 1024 / STAGE;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr int BAR_BYTES = 8 * (2 * S + 5) + 16;
+  static constexpr int SMEM = S * STAGE + BAR_BYTES + (int)sizeof(RowTable) + 1024 /* align slack */;
+  static_assert(SMEM <= 227 * 1024 && S >= 4, "shared memory of one CTA per SM");
+};
+
+template <int MODE, int NA>
+__global__ void __launch_bounds__(PairCfg<MODE, NA>::THREADS, 1)
+    lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                    const LinParams p) {
+  using C = PairCfg<MODE, NA>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::S * C::STAGE);   // (the leader's: both CTAs' copies landed)
+  uint64_t* sfree = full + C::S;     // stage consumed
+  uint64_t* accf = sfree + C::S;     // [2] accumulator ready
+  uint64_t* acce = accf + 2;         // [2] (the leader's) accumulator read by both CTAs' epilogues
+  uint64_t* drain = acce + 2;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  RowTable* tab = reinterpret_cast<RowTable*>(s_tmem + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)ptx::cluster_ctarank();
+  const int unit0 = blockIdx.x / 2, units = gridDim.x / 2;
+
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < C::S; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&sfree[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&accf[b], 1);
+      ptx::mbar_init(&acce[b], 2 * C::EPI_WARPS);
+    }
+    ptx::mbar_init(drain, 1);
+    *s_abort = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tensormap(&tm_a);
+    ptx::prefetch_tensormap(&tm_b);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(s_tmem, 512);
+    ptx::tmem_relinquish_pair();
+    ptx::tc_fence_before();
+  }
+  if (warp == 2) build_table<MODE>(p, tab);
+  ptx::cluster_sync();   // the peer's copies, commits and arrivals find initialized barriers
+  ptx::tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int64_t n_items = tab->items;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------------- producer (each CTA its share)
+    int64_t g = 0;
+    bool stop = false, withheld = false;
+    for (int64_t item = unit0; item < n_items && !stop; item += units) {
+      const LinTile t = table_tile<MODE>(p, tab, item, 32, 256);
+      const int kb_all = (t.clen + kBK - 1) / kBK, half = t.nw / 2, nbox = (half + 63) / 64;
+      for (int kb = 0; kb < kb_all; ++kb, ++g) {
+        const int s = (int)(g % C::S);
+        bool ok = true;
+        if (g >= C::S) ok = ptx::mbar_wait_bounded(&sfree[s], (uint32_t)(g / C::S - 1) & 1, s_abort, kWaitNs);
+        if (!__all_sync(0xffffffffu, ok)) {
+          stop = true;
+          break;
+        }
+        if (p.inject_timeout && unit0 == 0 && g == 0) {
+          withheld = true;   // test hook: this stage never fills
+          continue;
+        }
+        if (ptx::elect_one()) {
+          uint8_t* a = smem + s * C::STAGE;
+          uint8_t* b = a + NA * C::A_PANEL;
+          const uint32_t bar = ptx::mapa_shared(&full[s], 0);
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * (NA * C::A_PANEL + nbox * 8192));
+          const int c = kb * kBK, i0 = t.i0 + 128 * rank, j0 = t.j0 + half * rank;
+          if (MODE == kForward) {
+#pragma unroll
+            for (int h = 0; h < NA; ++h)
+              ptx::tma_load_2d_pair(a + h * C::A_PANEL, &tm_a, c, t.e * p.a_rows + h * p.I + i0, bar);
+          } else if (MODE == kInputGrad) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ptx::tma_load_3d_pair(a + h * 8192, &tm_a, i0 + 64 * h, c, t.e, bar);
+          }
+          if (MODE == kWeightGrad) {
+            const int d1 = tail_shift(t.clen - c), d2 = t.c0 + c;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) ptx::tma_load_3d_pair(a + h * 8192, &tm_a, i0 + 64 * h, d1, d2, bar);
+            for (int h = 0; h < nbox; ++h) ptx::tma_load_3d_pair(b + h * 8192, &tm_b, j0 + 64 * h, d1, d2, bar);
+          } else {
+            for (int h = 0; h < nbox; ++h) ptx::tma_load_2d_pair(b + h * 8192, &tm_b, c, j0 + 64 * h, bar);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // both CTAs' copies complete on the leader's barriers: it waits (bounded) for the last fill
+    // of every slot, and the cluster barrier at the end holds the peer until it has
+    if (rank == 0) {
+      volatile int local_abort = 0;
+      for (int64_t q = (g > C::S ? g - C::S : 0); q < g; ++q) {
+        if (withheld && q == 0) continue;
+        ptx::mbar_wait_bounded(&full[q % C::S], (uint32_t)(q / C::S) & 1, &local_abort, kWaitNs);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------------------------------------------------------- MMA issuer (the leader's)
+    if (rank == 0) {
+      constexpr uint64_t kStepA = C::A_MN ? 2048 >> 4 : 32 >> 4, kStepB = C::B_MN ? 2048 >> 4 : 32 >> 4;
+      int64_t g = 0;
+      int li = 0;
+      bool stop = false;
+      for (int64_t item = unit0; item < n_items && !stop; item += units, ++li) {
+        const LinTile t = table_tile<MODE>(p, tab, item, 32, 256);
+        const int kb_all = (t.clen + kBK - 1) / kBK, b2 = li & 1;
+        const uint32_t idesc = ptx::idesc_f16(p.bf16 != 0, 256, t.nw, C::A_MN, C::B_MN);
+        if (li >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait_cluster_bounded(
+                                                    &acce[b2], (uint32_t)((li >> 1) - 1) & 1, s_abort, kWaitNs)))
+          break;
+        ptx::tc_fence_after();
+        const uint32_t d = tmem + b2 * 256;
+        for (int kb = 0; kb < kb_all; ++kb, ++g) {
+          const int s = (int)(g % C::S);
+          if (!__all_sync(0xffffffffu,
+                          ptx::mbar_wait_bounded(&full[s], (uint32_t)(g / C::S) & 1, s_abort, kWaitNs))) {
+            stop = true;
+            break;
+          }
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint8_t* a = smem + s * C::STAGE;
+            const uint8_t* b = a + NA * C::A_PANEL;
+            const uint64_t da = C::A_MN ? ptx::smem_desc_mn_sw128(a) : ptx::smem_desc_k_sw128(a);
+            const uint64_t db = C::B_MN ? ptx::smem_desc_mn_sw128(b) : ptx::smem_desc_k_sw128(b);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+              for (int h = 0; h < NA; ++h)
+                ptx::mma_f16_ss_pair(d + h * C::NB, da + h * (C::A_PANEL >> 4) + k * kStepA, db + k * kStepB, idesc,
+                                     (kb | k) != 0);
+            }
+            ptx::tc_commit_pair(&sfree[s], (uint16_t)3);
+          }
+          __syncwarp();
+        }
+        if (!stop && ptx::elect_one()) ptx::tc_commit_pair(&accf[b2], (uint16_t)3);
+        __syncwarp();
+      }
+      if (ptx::elect_one()) ptx::tc_commit_pair(drain, (uint16_t)3);
+      __syncwarp();
+    }
+    volatile int local_abort = 0;
+    ptx::mbar_wait_bounded(drain, 0, &local_abort, kWaitNs);
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- epilogue warps
+    const int q = warp & 3, row = 32 * q + lane, part = (warp - 2) >> 2;
+    int li = 0;
+    for (int64_t item = unit0; item < n_items; item += units, ++li) {
+      const LinTile t = table_tile<MODE>(p, tab, item, 32, 256);
+      const int b2 = li & 1, i = t.i0 + 128 * rank + row;
+      const bool have = t.clen > 0;
+      float bias_a = 0.f, bias_b = 0.f;
+      if (MODE == kForward && p.bias && i < p.I) {
+        bias_a = __ldg(p.bias + (int64_t)t.e * p.a_rows + i);
+        if (NA == 2) bias_b = __ldg(p.bias + (int64_t)t.e * p.a_rows + p.I + i);
+      }
+      const bool ready = !*s_abort && ptx::mbar_wait_bounded(&accf[b2], (uint32_t)(li >> 1) & 1, s_abort, kWaitNs);
+      // (one answer for all epilogue warps: another role may raise the abort flag at any time)
+      if (ptx::bar_or<1, 32 * C::EPI_WARPS>(!ready)) break;
+      ptx::tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + b2 * 256;
+      auto release = [&] {   // this warp's reads are done: one arrival on the leader's barrier
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(&acce[b2], 0));
+      };
+      if (32 * part >= t.nw) release();
+      for (int c0 = 32 * part; c0 < t.nw; c0 += 64) {
+        uint32_t va[32], vb[32];
+        ptx::tmem_ld32(acc + c0, va);
+        if (NA == 2) ptx::tmem_ld32(acc + C::NB + c0, vb);
+        ptx::tmem_wait_ld();
+        if (c0 + 64 >= t.nw) release();
+        if (!have) {   // an expert without rows: the accumulator was never written
+#pragma unroll
+          for (int c = 0; c < 32; ++c) va[c] = vb[c] = 0u;
+        }
+        finish<MODE, NA>(p, t, va, vb, c0, i, bias_a, bias_b);
+      }
+    }
+  }
+
+  __syncthreads();
+  if (*s_abort && threadIdx.x == 0) set_status(p.status, MOE_ERR_TIMEOUT);
+  // the leader has seen every copy of both CTAs land and the MMAs complete before either CTA
+  // frees its TMEM and exits
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
 // ------------------------------------------------------------------------------ host side
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -647,18 +948,80 @@ int launch_split(const LinArgs& a) {
   return err == cudaSuccess ? 1 : -1;
 }
 
+// Clusters of two CTAs of `kern` that the device holds at once, remembered per device.
+template <class K>
+int pair_slots(K kern, int threads, int smem, std::atomic<int>* known) {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_acquire)) > 0) return n;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * multiprocessors());
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
+  if (dev < 64) known[dev].store(n, std::memory_order_release);
+  return n;
+}
+
+template <int MODE, int NA>
+int launch_pair(const LinArgs& a) {
+  using C = PairCfg<MODE, NA>;
+  CUtensorMap ma, mb;
+  if (!operand_maps(a, 128, 64, &ma, &mb)) return -1;
+  LinParams p = params_of(a, 256);
+  p.nw_max = C::NB;
+  p.n_jt = (a.N + C::NB - 1) / C::NB;
+  p.splits = 1;
+  auto kern = lin_pair_kernel<MODE, NA>;
+  static std::atomic<uint64_t> done{0};
+  static std::atomic<int> slots[64];
+  if (!allow_smem(kern, C::SMEM, done)) return -1;
+  const int n = pair_slots(kern, C::THREADS, C::SMEM, slots);
+  if (n <= 0) return -1;
+  const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, C::NB)) * p.n_it;
+  const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, n);
+  return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, false, 2u, ma, mb, p) ==
+                 cudaSuccess ? 1 : -1;
+}
+
+// Tiles of 256 x nw that the product makes (on average over the experts' counts).
+int64_t pair_tiles(const LinArgs& a, int nw) {
+  const int64_t I = a.mode != kForward ? a.K : a.fn == MOE_FN_SWIGLU ? a.N / 2 : a.N;
+  const int64_t j = a.mode == kWeightGrad ? a.E * (int64_t)((a.N + nw - 1) / nw)
+                    : a.offsets           ? std::min<int64_t>(a.E, a.rows) * ((a.rows / a.E + nw - 1) / nw)
+                                          : (a.rows + nw - 1) / nw;
+  return j * ((I + 255) / 256);
+}
+
 }  // namespace
 
 int launch_linear(const LinArgs& a) {
   const bool narrow = a.rows <= 32 * (a.offsets ? a.E : 1);   // few rows an expert: the weights' stream is the work
+  const bool swiglu = a.mode == kForward && a.fn == MOE_FN_SWIGLU;
+  // CTA pairs once their tiles fill about half of the SMs (fewer: smaller tiles on more SMs).
+  const bool pair = pair_tiles(a, swiglu ? 128 : 256) >= multiprocessors() / 4 && (a.mode == kWeightGrad || !narrow);
   switch (a.mode) {
     case kForward:
-      if (a.fn == MOE_FN_SWIGLU) return narrow ? launch_split<kForward, 2, 32>(a) : launch_split<kForward, 2, 128>(a);
-      return narrow ? launch_split<kForward, 1, 32>(a) : launch_split<kForward, 1, 128>(a);
+      if (swiglu)
+        return pair ? launch_pair<kForward, 2>(a) : narrow ? launch_split<kForward, 2, 32>(a)
+                                                           : launch_split<kForward, 2, 128>(a);
+      return pair ? launch_pair<kForward, 1>(a) : narrow ? launch_split<kForward, 1, 32>(a)
+                                                         : launch_split<kForward, 1, 128>(a);
     case kInputGrad:
-      return narrow ? launch_split<kInputGrad, 1, 32>(a) : launch_split<kInputGrad, 1, 128>(a);
+      return pair ? launch_pair<kInputGrad, 1>(a) : narrow ? launch_split<kInputGrad, 1, 32>(a)
+                                                           : launch_split<kInputGrad, 1, 128>(a);
     default:
-      return launch_split<kWeightGrad, 1, 128>(a);
+      return pair ? launch_pair<kWeightGrad, 1>(a) : launch_split<kWeightGrad, 1, 128>(a);
   }
 }
 

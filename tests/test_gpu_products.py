@@ -34,6 +34,9 @@ FORWARD = [
     (700, 4096, 128, "silu", BF, True, False, False),
     (1031, 512, 2880, "gelu_tanh", HF, True, True, False),
     (2500, 192, 640, "swiglu", BF, True, True, True),
+    (2111, 2880, 1304, "none", BF, True, True, True),
+    (4096, 72, 5760, "swiglu", HF, True, False, True),
+    (3000, 1024, 4096, "gelu", BF, False, False, False),
 ]
 
 
@@ -111,6 +114,9 @@ BACKWARD = [
     (200, 2880, 96, "none", HF, True),
     (1000, 192, 320, "gelu_tanh", HF, False),
     (4099, 320, 192, "swiglu", BF, True),
+    (2000, 2888, 1304, "silu", BF, True),
+    (777, 2880, 5760, "swiglu", HF, True),
+    (70, 4096, 2048, "none", BF, True),
 ]
 
 
@@ -188,6 +194,9 @@ GROUPED = [
     ([0] * 255 + [17], 1, 0, 64, 128, "none", HF),
     ([0, 0, 0], 6, 0, 64, 64, "none", BF),
     ([3, 1, 4, 1, 5, 9, 2, 6] * 32, 0, 0, 128, 640, "swiglu", BF),
+    ([0, 500, 1, 33, 0, 129, 700, 256], 5, 3, 1032, 2576, "swiglu", BF),
+    ([130, 0, 600, 257, 31, 0, 64, 1000], 0, 0, 2880, 1096, "none", HF),
+    ([97] * 20 + [0] * 3 + [300], 2, 0, 520, 1544, "gelu", BF),
 ]
 
 
