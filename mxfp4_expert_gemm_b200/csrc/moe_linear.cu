@@ -62,11 +62,22 @@ struct LinTile {
 };
 
 // ------------------------------------------------------------------------------ conversions
-__device__ __forceinline__ uint16_t to16(float v, bool bf) {
-  return bf ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+template <bool BF>
+__device__ __forceinline__ uint16_t to16(float v) {
+  return BF ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
 }
-__device__ __forceinline__ float from16(uint16_t v, bool bf) {
-  return bf ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+template <bool BF>
+__device__ __forceinline__ uint32_t to16x2(float lo, float hi) {   // lo in the low half
+  if (BF) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <bool BF>
+__device__ __forceinline__ float from16(uint16_t v) {
+  return BF ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
 }
 
 // ------------------------------------------------------------------------------ activations
@@ -308,96 +319,189 @@ __device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable
 __device__ __forceinline__ int tail_shift(int n) { return n < kBK ? n - kBK : 0; }
 
 // ------------------------------------------------------------------------------ epilogue
-// One accumulator value (NA = 2: the gate's and the up's) to the outputs at (row, i).
-template <int FN>
-__device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t, const uint32_t (&va)[32],
-                                            const uint32_t (&vb)[32], int col0, int i, float bias_a, float bias_b) {
-  const bool bf = p.bf16 != 0;
-  if (i >= p.I) return;
-  const int n = min(32, t.nj - col0);   // valid columns (may be <= 0)
-  uint16_t* out = p.out + t.e * p.out_expert + i;
-  uint16_t* z = p.z ? p.z + i : nullptr;
-  const int64_t ldz = (FN == MOE_FN_SWIGLU ? 2 : 1) * (int64_t)p.I;
-  uint16_t res[32];
-  if (p.residual) {
-    const uint16_t* r = p.residual + i;
+// Four warps (128 threads, named barrier `bar`) finish 32 columns of a tile: thread `row` holds
+// the fp32 values of TMEM lane `row` (column col0 + c in v[c]).  Lanes run along an output row,
+// so the 16-bit results pass through a [32][128] shared buffer and leave as 16-byte stores,
+// 256 bytes of an output row by 16 threads (64-byte stores straight from the lanes ran a weight
+// gradient's stores at 1.3 TB/s).
+// SwiGLU: lanes 0-63 hold the gate and lanes 64-127 the up values of the tile's 64 features; the
+// up lanes hand their values of columns 0-15 to the gate lanes, and take the gate values of
+// columns 16-31 from them, so that every thread finishes 16 columns.
+constexpr int kEpiBytes = 8192;
+
+__device__ __forceinline__ void group_sync(int bar) { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); }
+
+// Rows c < n of a [32][W] 16-bit buffer to dst (row c at dst + c ld), columns < lim.
+template <int W>
+__device__ __forceinline__ void store_rows(const LinParams& p, const uint8_t* buf, uint16_t* dst, int64_t ld, int n,
+                                           int lim, int th, const uint16_t* lo, const uint16_t* hi) {
+  constexpr int V = W / 8;              // 16-byte pieces per row
+  const int v = th % V;
+  if (8 * v >= lim) return;             // (lim is a multiple of 8)
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-      if (c < n) res[c] = r[(int64_t)(t.j0 + col0 + c) * p.ld_res];   // (y may be this buffer: no read-only path)
-  }
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    if (c >= n) break;
-    const int64_t row = t.j0 + col0 + c;
-    const float a = __uint_as_float(va[c]) + bias_a;
-    float y;
-    if (FN == MOE_FN_SWIGLU) {
-      const float u = __uint_as_float(vb[c]) + bias_b;
-      if (z) {
-        uint16_t* q = z + row * ldz;
-        if (in_bounds(q + p.I, p.z, p.z_end, p.status)) {
-          q[0] = to16(a, bf);
-          q[p.I] = to16(u, bf);
-        }
-      }
-      y = swiglu(a, u, p.limit);
-    } else {
-      if (z) {
-        uint16_t* q = z + row * ldz;
-        if (in_bounds(q, p.z, p.z_end, p.status)) *q = to16(a, bf);
-      }
-      y = act_fn<FN>(a);
+  for (int c = th / V; c < 32; c += 128 / V) {
+    if (c < n) {
+      uint4* q = reinterpret_cast<uint4*>(dst + c * ld + 8 * v);
+      const uint4 val = *reinterpret_cast<const uint4*>(buf + c * (2 * W) + 16 * v);
+      if (in_bounds(q, lo, hi, p.status)) *q = val;
     }
-    if (p.residual) y += from16(res[c], bf);
-    uint16_t* q = out + row * p.ld_out;
-    if (in_bounds(q, p.out, p.out_end, p.status)) *q = to16(y, bf);
   }
 }
 
-template <int MODE, int NA>
-__device__ __forceinline__ void finish(const LinParams& p, const LinTile& t, const uint32_t (&va)[32],
-                                       const uint32_t (&vb)[32], int col0, int i, float bias_a, float bias_b) {
-  if (NA == 2) return finish_cols<MOE_FN_SWIGLU>(p, t, va, vb, col0, i, bias_a, bias_b);
+template <int W>
+__device__ __forceinline__ void load_rows(uint8_t* buf, const uint16_t* src, int64_t ld, int n, int lim, int th) {
+  constexpr int V = W / 8;
+  const int v = th % V;
+  if (8 * v >= lim) return;
+#pragma unroll
+  for (int c = th / V; c < 32; c += 128 / V)
+    if (c < n) *reinterpret_cast<uint4*>(buf + c * (2 * W) + 16 * v) = *reinterpret_cast<const uint4*>(src + c * ld + 8 * v);
+}
+
+// 16-bit values of 32 columns into the buffer, each thread its lane's.
+template <bool BF>
+__device__ __forceinline__ void stage_lane(uint8_t* buf, const float (&v)[32], int row) {
+  uint16_t* b = reinterpret_cast<uint16_t*>(buf) + row;
+#pragma unroll
+  for (int c = 0; c < 32; c += 2) {
+    const uint32_t w = to16x2<BF>(v[c], v[c + 1]);
+    b[c * 128] = (uint16_t)w;
+    b[(c + 1) * 128] = (uint16_t)(w >> 16);
+  }
+}
+
+template <int FN, bool BF>
+__device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t, float (&v)[32], int col0, int row,
+                                            uint8_t* buf, int bar) {
+  const int n = min(32, t.nj - col0);   // valid columns
+  const int64_t r0 = t.j0 + col0;
+  uint16_t* out = p.out + t.e * p.out_expert + r0 * p.ld_out + t.i0;
+  const int lim = p.I - t.i0;           // columns of out from i0 on
+  group_sync(bar);                      // the buffer's last readers are done
+  if (p.z) {
+    stage_lane<BF>(buf, v, row);
+    group_sync(bar);
+    if (FN == MOE_FN_SWIGLU) {
+      const int64_t ldz = 2 * (int64_t)p.I;
+      // gate lanes' 64 columns to z's first half, up lanes' to its second
+      const int h = row >> 6;
+      const uint8_t* hb = buf + 128 * h;
+      uint16_t* dst = p.z + r0 * ldz + h * (int64_t)p.I + t.i0;
+      const int w = row & 63, vv = w & 7;
+      if (8 * vv < lim) {
+#pragma unroll
+        for (int c = w >> 3; c < 32; c += 8)
+          if (c < n) {
+            uint4* q = reinterpret_cast<uint4*>(dst + c * ldz + 8 * vv);
+            if (in_bounds(q, p.z, p.z_end, p.status)) *q = *reinterpret_cast<const uint4*>(hb + c * 256 + 16 * vv);
+          }
+      }
+    } else {
+      store_rows<128>(p, buf, p.z + r0 * p.I + t.i0, p.I, n, lim, row, p.z, p.z_end);
+    }
+    group_sync(bar);
+  }
+  if (FN == MOE_FN_SWIGLU) {
+    const bool up = row >= 64;
+    const int f = row & 63;
+    float* ex = reinterpret_cast<float*>(buf);   // [2][16][64]: u of columns 0-15, g of columns 16-31
+#pragma unroll
+    for (int c = 0; c < 16; ++c) ex[((up ? 0 : 16) + c) * 64 + f] = up ? v[c] : v[16 + c];
+    group_sync(bar);
+    float y[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float o = ex[((up ? 16 : 0) + c) * 64 + f];
+      y[c] = up ? swiglu(o, v[16 + c], p.limit) : swiglu(v[c], o, p.limit);
+    }
+    group_sync(bar);
+    uint16_t* b = reinterpret_cast<uint16_t*>(buf) + (up ? 16 * 64 : 0) + f;
+    if (p.residual) {
+      load_rows<64>(buf + 4096, p.residual + r0 * p.ld_res + t.i0, p.ld_res, n, lim, row);
+      group_sync(bar);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) y[c] += from16<BF>(b[2048 + c * 64]);
+    }
+#pragma unroll
+    for (int c = 0; c < 16; c += 2) {
+      const uint32_t w = to16x2<BF>(y[c], y[c + 1]);
+      b[c * 64] = (uint16_t)w;
+      b[(c + 1) * 64] = (uint16_t)(w >> 16);
+    }
+    group_sync(bar);
+    store_rows<64>(p, buf, out, p.ld_out, n, lim, row, p.out, p.out_end);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = act_fn<FN>(v[c]);
+    if (p.residual) {
+      load_rows<128>(buf, p.residual + r0 * p.ld_res + t.i0, p.ld_res, n, lim, row);
+      group_sync(bar);
+      const uint16_t* b = reinterpret_cast<const uint16_t*>(buf) + row;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) v[c] += from16<BF>(b[c * 128]);   // (read, then overwritten, by this thread alone)
+    }
+    stage_lane<BF>(buf, v, row);
+    group_sync(bar);
+    store_rows<128>(p, buf, out, p.ld_out, n, lim, row, p.out, p.out_end);
+  }
+}
+
+// acc: the raw accumulator values; bias: this lane's.
+template <int MODE, bool SW, bool BF>
+__device__ __forceinline__ void finish(const LinParams& p, const LinTile& t, const uint32_t (&acc)[32], float bias,
+                                       int col0, int row, uint8_t* buf, int bar) {
+  if (col0 >= t.nj) return;   // (the same for the whole group)
+  float v[32];
+#pragma unroll
+  for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(acc[c]) + bias;
+  if (SW) return finish_cols<MOE_FN_SWIGLU, BF>(p, t, v, col0, row, buf, bar);
   if (MODE == kForward) {
     switch (p.fn) {
-      case MOE_FN_RELU: return finish_cols<MOE_FN_RELU>(p, t, va, vb, col0, i, bias_a, bias_b);
-      case MOE_FN_GELU: return finish_cols<MOE_FN_GELU>(p, t, va, vb, col0, i, bias_a, bias_b);
-      case MOE_FN_GELU_TANH: return finish_cols<MOE_FN_GELU_TANH>(p, t, va, vb, col0, i, bias_a, bias_b);
-      case MOE_FN_SILU: return finish_cols<MOE_FN_SILU>(p, t, va, vb, col0, i, bias_a, bias_b);
+      case MOE_FN_RELU: return finish_cols<MOE_FN_RELU, BF>(p, t, v, col0, row, buf, bar);
+      case MOE_FN_GELU: return finish_cols<MOE_FN_GELU, BF>(p, t, v, col0, row, buf, bar);
+      case MOE_FN_GELU_TANH: return finish_cols<MOE_FN_GELU_TANH, BF>(p, t, v, col0, row, buf, bar);
+      case MOE_FN_SILU: return finish_cols<MOE_FN_SILU, BF>(p, t, v, col0, row, buf, bar);
     }
   }
-  finish_cols<MOE_FN_NONE>(p, t, va, vb, col0, i, bias_a, bias_b);
+  finish_cols<MOE_FN_NONE, BF>(p, t, v, col0, row, buf, bar);
+}
+
+// This lane's bias (SwiGLU: lanes 0-63 the gate's, 64-127 the up's).
+template <int MODE, bool SW>
+__device__ __forceinline__ float lane_bias(const LinParams& p, const LinTile& t, int row) {
+  if (MODE != kForward || !p.bias) return 0.f;
+  const int i = t.i0 + (SW ? row & 63 : row);
+  return i < p.I ? __ldg(p.bias + (int64_t)t.e * p.a_rows + (SW && row >= 64 ? p.I : 0) + i) : 0.f;
 }
 
 // ------------------------------------------------------------------------------ split kernel
 // One CTA (or a cluster of `splits` CTAs that share a tile's contraction) per output tile of
-// 128 i x at most NB j (NA = 2: 128 gate and the matching 128 up features).
-template <int MODE, int NA, int NB>
+// 128 i x at most NB j (SwiGLU: 64 gate and the matching 64 up features).
+template <int MODE, int NB>
 struct SplitCfg {
   static constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeightGrad;
   static constexpr int A_PANEL = 128 * 128;             // 128 i x 64 c of 2 bytes
   static constexpr int B_BOX = NB < 64 ? NB : 64;       // j per copy of B
   static constexpr int B_BYTES = NB * 128;
-  static constexpr int STAGE = NA * A_PANEL + B_BYTES;
-  static constexpr int CPS = (NA == 2 && NB == 128) ? 1 : 2;   // CTAs per SM
-  static constexpr int S = ((CPS == 1 ? 200 : 108) * 1024) / STAGE > 6 ? 6 : ((CPS == 1 ? 200 : 108) * 1024) / STAGE;
-  static constexpr int COLS = NA * NB;
-  static constexpr int TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : 256;
-  static constexpr int RED_BYTES = COLS * 128 * 4;      // fp32 partial tile (reuses the stages)
+  static constexpr int STAGE = A_PANEL + B_BYTES;
+  static constexpr int CPS = 2;                         // CTAs per SM
+  static constexpr int S = 108 * 1024 / STAGE;
+  static constexpr int TMEM_COLS = NB;
+  static constexpr int RED_BYTES = NB * 128 * 4;        // fp32 partial tile, and the epilogue's
+  static constexpr int EPI_OFF = RED_BYTES;             // buffer: both reuse the stages
   static constexpr int BAR_BYTES = 8 * (2 * S + 2) + 64;
   static constexpr int SMEM = S * STAGE + BAR_BYTES + 1024 /* align slack */;
   static constexpr int THREADS = 32 * 6;                // producer, MMA, four epilogue warps
-  static_assert(RED_BYTES <= S * STAGE, "the partial tile fits the stages");
+  static_assert(RED_BYTES + kEpiBytes <= S * STAGE, "the partial tile and the epilogue's buffer fit the stages");
   static_assert((SMEM + 1024) * CPS <= 228 * 1024, "shared memory of the co-resident CTAs");
-  static_assert(COLS * CPS <= 512, "TMEM of the co-resident CTAs");
-  static_assert(NB % 32 == 0 && NB <= 256 && (!B_MN || NB % 64 == 0), "tile width");
+  static_assert((NB == 32 || NB == 64 || NB == 128) && (!B_MN || NB % 64 == 0), "tile width");
 };
 
-template <int MODE, int NA, int NB>
-__global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE, NA, NB>::CPS)
+template <int MODE, bool SW, int NB, bool BF>
+__global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB>::CPS)
     lin_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const LinParams p) {
-  using C = SplitCfg<MODE, NA, NB>;
+  using C = SplitCfg<MODE, NB>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::S * C::STAGE);
@@ -431,7 +535,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE
     ptx::tc_fence_before();
   }
   if (warp == 2) {
-    const LinTile t = find_tile<MODE, true>(p, item, 16, 128);
+    const LinTile t = find_tile<MODE, true>(p, item, 16, SW ? 64 : 128);
     if (lane == 0) *s_tile = t;
   }
   __syncthreads();
@@ -457,13 +561,13 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE
       }
       if (ptx::elect_one()) {
         uint8_t* a = smem + s * C::STAGE;
-        uint8_t* b = a + NA * C::A_PANEL;
-        ptx::mbar_arrive_expect_tx(&full[s], NA * C::A_PANEL + nbox * C::B_BOX * 128);
+        uint8_t* b = a + C::A_PANEL;
+        ptx::mbar_arrive_expect_tx(&full[s], C::A_PANEL + nbox * C::B_BOX * 128);
         const int c = kb * kBK;
         if (MODE == kForward) {
-#pragma unroll
-          for (int h = 0; h < NA; ++h)
-            ptx::tma_load_2d(a + h * C::A_PANEL, &tm_a, c, t.e * p.a_rows + h * p.I + t.i0, &full[s]);
+          const int arow = t.e * p.a_rows + t.i0;
+          ptx::tma_load_2d(a, &tm_a, c, arow, &full[s]);
+          if (SW) ptx::tma_load_2d(a + 8192, &tm_a, c, arow + p.I, &full[s]);   // (boxes of 64 rows)
         } else if (MODE == kInputGrad) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) ptx::tma_load_3d(a + h * 8192, &tm_a, t.i0 + 64 * h, c, t.e, &full[s]);
@@ -489,7 +593,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE
     __syncwarp();
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer
-    const uint32_t idesc = ptx::idesc_f16(p.bf16 != 0, 128, t.nw, C::A_MN, C::B_MN);
+    const uint32_t idesc = ptx::idesc_f16(BF, 128, t.nw, C::A_MN, C::B_MN);
     // a 16-wide step of c: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
     constexpr uint64_t kStepA = C::A_MN ? 2048 >> 4 : 32 >> 4, kStepB = C::B_MN ? 2048 >> 4 : 32 >> 4;
     int g = 0;
@@ -504,16 +608,11 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE
       ptx::tc_fence_after();
       if (ptx::elect_one()) {
         const uint8_t* a = smem + s * C::STAGE;
-        const uint8_t* b = a + NA * C::A_PANEL;
+        const uint8_t* b = a + C::A_PANEL;
         const uint64_t da = C::A_MN ? ptx::smem_desc_mn_sw128(a) : ptx::smem_desc_k_sw128(a);
         const uint64_t db = C::B_MN ? ptx::smem_desc_mn_sw128(b) : ptx::smem_desc_k_sw128(b);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-#pragma unroll
-          for (int h = 0; h < NA; ++h)
-            ptx::mma_f16_ss(tmem + h * NB, da + h * (C::A_PANEL >> 4) + k * kStepA, db + k * kStepB, idesc,
-                            (g | k) != 0);
-        }
+        for (int k = 0; k < 4; ++k) ptx::mma_f16_ss(tmem, da + k * kStepA, db + k * kStepB, idesc, (g | k) != 0);
         ptx::tc_commit(&sfree[s]);
       }
       __syncwarp();
@@ -528,35 +627,27 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE
     __syncwarp();
   } else {
     // ---------------------------------------------------------------- epilogue warps
-    const int q = warp & 3, row = 32 * q + lane, i = t.i0 + row;
+    const int q = warp & 3, row = 32 * q + lane;
     const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
     const bool have = kb1 > kb0;
     const bool ready = ptx::mbar_wait_bounded(accf, 0, s_abort, kWaitNs);
     if (!ptx::bar_or<1, 128>(!ready) && t.ok) {
       ptx::tc_fence_after();
-      float bias_a = 0.f, bias_b = 0.f;
-      if (MODE == kForward && p.bias && i < p.I) {
-        bias_a = __ldg(p.bias + (int64_t)t.e * p.a_rows + i);
-        if (NA == 2) bias_b = __ldg(p.bias + (int64_t)t.e * p.a_rows + p.I + i);
-      }
+      const float bias = lane_bias<MODE, SW>(p, t, row);
       float* red = reinterpret_cast<float*>(smem);
       for (int c0 = 0; c0 < t.nw; c0 += 32) {
-        uint32_t va[32], vb[32];
-        ptx::tmem_ld32(acc + c0, va);
-        if (NA == 2) ptx::tmem_ld32(acc + NB + c0, vb);
+        uint32_t v[32];
+        ptx::tmem_ld32(acc + c0, v);
         ptx::tmem_wait_ld();
         if (!have) {   // no contraction block here: the accumulator was never written
 #pragma unroll
-          for (int c = 0; c < 32; ++c) va[c] = vb[c] = 0u;
+          for (int c = 0; c < 32; ++c) v[c] = 0u;
         }
         if (S == 1) {
-          finish<MODE, NA>(p, t, va, vb, c0, i, bias_a, bias_b);
+          finish<MODE, SW, BF>(p, t, v, bias, c0, row, smem + C::EPI_OFF, 2);
         } else {
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            red[(c0 + c) * 128 + row] = __uint_as_float(va[c]);
-            if (NA == 2) red[(NB + c0 + c) * 128 + row] = __uint_as_float(vb[c]);
-          }
+          for (int c = 0; c < 32; ++c) red[(c0 + c) * 128 + row] = __uint_as_float(v[c]);
         }
       }
     }
@@ -566,35 +657,29 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE
   if (*s_abort && threadIdx.x == 0) set_status(p.status, MOE_ERR_TIMEOUT);
   if (S > 1) {
     // The cluster's partial tiles meet over distributed shared memory: CTA r adds and finishes
-    // its share of the columns, in rank order, so that the sum does not depend on timing.
+    // its share of the columns, in rank order, so that the sum does not depend on timing.  A
+    // rank's 32 loads per thread are issued together (one after another they took 40 us).
     ptx::cluster_sync();
     if (warp >= 2 && t.ok) {
-      const int q = warp & 3, row = 32 * q + lane, i = t.i0 + row;
-      float bias_a = 0.f, bias_b = 0.f;
-      if (MODE == kForward && p.bias && i < p.I) {
-        bias_a = __ldg(p.bias + (int64_t)t.e * p.a_rows + i);
-        if (NA == 2) bias_b = __ldg(p.bias + (int64_t)t.e * p.a_rows + p.I + i);
-      }
+      const int row = 32 * (warp & 3) + lane;
+      const float bias = lane_bias<MODE, SW>(p, t, row);
       const int per = (t.nw + S - 1) / S;   // columns per CTA
       const int c1 = min((rank + 1) * per, t.nj);
+      LinTile mine = t;
+      mine.nj = c1;
       for (int c0 = rank * per; c0 < c1; c0 += 32) {
-        uint32_t va[32], vb[32];
-        LinTile tt = t;
-        tt.nj = c1;
-        const int n = min(32, c1 - c0);
+        uint32_t v[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float sa = 0.f, sb = 0.f;
-          if (c < n) {
-            for (int r = 0; r < S; ++r) {
-              sa += ptx::ld_cluster_f32(ptx::mapa_shared(smem + ((c0 + c) * 128 + row) * 4, r));
-              if (NA == 2) sb += ptx::ld_cluster_f32(ptx::mapa_shared(smem + ((NB + c0 + c) * 128 + row) * 4, r));
-            }
-          }
-          va[c] = __float_as_uint(sa);
-          vb[c] = __float_as_uint(sb);
+        for (int c = 0; c < 32; ++c) v[c] = 0u;
+        for (int r = 0; r < S; ++r) {
+          const uint32_t peer = ptx::mapa_shared(smem + (c0 * 128 + row) * 4, r);
+          float w[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) w[c] = c0 + c < c1 ? ptx::ld_cluster_f32(peer + c * 512) : 0.f;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) + w[c]);
         }
-        finish<MODE, NA>(p, tt, va, vb, c0, i, bias_a, bias_b);
+        finish<MODE, SW, BF>(p, mine, v, bias, c0, row, smem + C::EPI_OFF, 2);
       }
     }
     ptx::cluster_sync();   // no CTA leaves while a peer reads its partial tile
@@ -607,33 +692,34 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NA, NB>::THREADS, SplitCfg<MODE
 
 // ------------------------------------------------------------------------------ pair kernel
 // Large products: persistent CTA pairs (cta_group::2, one MMA of M = 256 over two SMs), tiles of
-// 256 i x at most 256 j (NA = 2: 256 gate and the matching 256 up features x at most 128 j).
-// Each CTA holds its 128 rows of A (and of the second accumulator's A) and half of B's rows, so a
-// pair moves half the bytes into shared memory per multiply-add that two single CTAs would.  The
+// 256 i x at most 256 j (SwiGLU: in each CTA 64 gate and the matching 64 up features).  Each CTA
+// holds its 128 rows of A and half of B's rows, so a pair moves half the bytes into shared memory
+// per multiply-add that two single CTAs would.  The
 // accumulator is double-buffered in TMEM: the epilogue of a tile runs under the next tile's MMAs.
-template <int MODE, int NA>
+template <int MODE>
 struct PairCfg {
   static constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeightGrad;
-  static constexpr int NB = 256 / NA;                   // widest tile along j
+  static constexpr int NB = 256;                        // widest tile along j
   static constexpr int A_PANEL = 128 * 128;
   static constexpr int B_BYTES = NB / 2 * 128;          // this CTA's half of B
-  static constexpr int STAGE = NA * A_PANEL + B_BYTES;
-  static constexpr int S = 200 * 1024 / STAGE;
+  static constexpr int STAGE = A_PANEL + B_BYTES;
+  static constexpr int S = 6;
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = 32 * (2 + EPI_WARPS);
   static constexpr int BAR_BYTES = 8 * (2 * S + 5) + 16;
-  static constexpr int SMEM = S * STAGE + BAR_BYTES + (int)sizeof(RowTable) + 1024 /* align slack */;
+  static constexpr int SMEM = S * STAGE + 2 * kEpiBytes + BAR_BYTES + (int)sizeof(RowTable) + 1024 /* align slack */;
   static_assert(SMEM <= 227 * 1024 && S >= 4, "shared memory of one CTA per SM");
 };
 
-template <int MODE, int NA>
-__global__ void __launch_bounds__(PairCfg<MODE, NA>::THREADS, 1)
+template <int MODE, bool SW, bool BF>
+__global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                     const LinParams p) {
-  using C = PairCfg<MODE, NA>;
+  using C = PairCfg<MODE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::S * C::STAGE);   // (the leader's: both CTAs' copies landed)
+  uint8_t* epi = smem + C::S * C::STAGE;
+  uint64_t* full = reinterpret_cast<uint64_t*>(epi + 2 * kEpiBytes);   // (the leader's: both CTAs' copies landed)
   uint64_t* sfree = full + C::S;     // stage consumed
   uint64_t* accf = sfree + C::S;     // [2] accumulator ready
   uint64_t* acce = accf + 2;         // [2] (the leader's) accumulator read by both CTAs' epilogues
@@ -643,6 +729,7 @@ __global__ void __launch_bounds__(PairCfg<MODE, NA>::THREADS, 1)
   RowTable* tab = reinterpret_cast<RowTable*>(s_tmem + 4);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kIW = SW ? 128 : 256;   // columns of out per tile
   const int rank = (int)ptx::cluster_ctarank();
   const int unit0 = blockIdx.x / 2, units = gridDim.x / 2;
 
@@ -677,7 +764,7 @@ __global__ void __launch_bounds__(PairCfg<MODE, NA>::THREADS, 1)
     int64_t g = 0;
     bool stop = false, withheld = false;
     for (int64_t item = unit0; item < n_items && !stop; item += units) {
-      const LinTile t = table_tile<MODE>(p, tab, item, 32, 256);
+      const LinTile t = table_tile<MODE>(p, tab, item, 32, kIW);
       const int kb_all = (t.clen + kBK - 1) / kBK, half = t.nw / 2, nbox = (half + 63) / 64;
       for (int kb = 0; kb < kb_all; ++kb, ++g) {
         const int s = (int)(g % C::S);
@@ -693,14 +780,14 @@ __global__ void __launch_bounds__(PairCfg<MODE, NA>::THREADS, 1)
         }
         if (ptx::elect_one()) {
           uint8_t* a = smem + s * C::STAGE;
-          uint8_t* b = a + NA * C::A_PANEL;
+          uint8_t* b = a + C::A_PANEL;
           const uint32_t bar = ptx::mapa_shared(&full[s], 0);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * (NA * C::A_PANEL + nbox * 8192));
-          const int c = kb * kBK, i0 = t.i0 + 128 * rank, j0 = t.j0 + half * rank;
+          if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * (C::A_PANEL + nbox * 8192));
+          const int c = kb * kBK, i0 = t.i0 + kIW / 2 * rank, j0 = t.j0 + half * rank;
           if (MODE == kForward) {
-#pragma unroll
-            for (int h = 0; h < NA; ++h)
-              ptx::tma_load_2d_pair(a + h * C::A_PANEL, &tm_a, c, t.e * p.a_rows + h * p.I + i0, bar);
+            const int arow = t.e * p.a_rows + i0;
+            ptx::tma_load_2d_pair(a, &tm_a, c, arow, bar);
+            if (SW) ptx::tma_load_2d_pair(a + 8192, &tm_a, c, arow + p.I, bar);   // (boxes of 64 rows)
           } else if (MODE == kInputGrad) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) ptx::tma_load_3d_pair(a + h * 8192, &tm_a, i0 + 64 * h, c, t.e, bar);
@@ -735,9 +822,9 @@ __global__ void __launch_bounds__(PairCfg<MODE, NA>::THREADS, 1)
       int li = 0;
       bool stop = false;
       for (int64_t item = unit0; item < n_items && !stop; item += units, ++li) {
-        const LinTile t = table_tile<MODE>(p, tab, item, 32, 256);
+        const LinTile t = table_tile<MODE>(p, tab, item, 32, kIW);
         const int kb_all = (t.clen + kBK - 1) / kBK, b2 = li & 1;
-        const uint32_t idesc = ptx::idesc_f16(p.bf16 != 0, 256, t.nw, C::A_MN, C::B_MN);
+        const uint32_t idesc = ptx::idesc_f16(BF, 256, t.nw, C::A_MN, C::B_MN);
         if (li >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait_cluster_bounded(
                                                     &acce[b2], (uint32_t)((li >> 1) - 1) & 1, s_abort, kWaitNs)))
           break;
@@ -753,16 +840,12 @@ __global__ void __launch_bounds__(PairCfg<MODE, NA>::THREADS, 1)
           ptx::tc_fence_after();
           if (ptx::elect_one()) {
             const uint8_t* a = smem + s * C::STAGE;
-            const uint8_t* b = a + NA * C::A_PANEL;
+            const uint8_t* b = a + C::A_PANEL;
             const uint64_t da = C::A_MN ? ptx::smem_desc_mn_sw128(a) : ptx::smem_desc_k_sw128(a);
             const uint64_t db = C::B_MN ? ptx::smem_desc_mn_sw128(b) : ptx::smem_desc_k_sw128(b);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-              for (int h = 0; h < NA; ++h)
-                ptx::mma_f16_ss_pair(d + h * C::NB, da + h * (C::A_PANEL >> 4) + k * kStepA, db + k * kStepB, idesc,
-                                     (kb | k) != 0);
-            }
+            for (int k = 0; k < 4; ++k)
+              ptx::mma_f16_ss_pair(d, da + k * kStepA, db + k * kStepB, idesc, (kb | k) != 0);
             ptx::tc_commit_pair(&sfree[s], (uint16_t)3);
           }
           __syncwarp();
@@ -781,14 +864,11 @@ __global__ void __launch_bounds__(PairCfg<MODE, NA>::THREADS, 1)
     const int q = warp & 3, row = 32 * q + lane, part = (warp - 2) >> 2;
     int li = 0;
     for (int64_t item = unit0; item < n_items; item += units, ++li) {
-      const LinTile t = table_tile<MODE>(p, tab, item, 32, 256);
-      const int b2 = li & 1, i = t.i0 + 128 * rank + row;
+      LinTile t = table_tile<MODE>(p, tab, item, 32, kIW);
+      t.i0 += kIW / 2 * rank;
+      const int b2 = li & 1;
       const bool have = t.clen > 0;
-      float bias_a = 0.f, bias_b = 0.f;
-      if (MODE == kForward && p.bias && i < p.I) {
-        bias_a = __ldg(p.bias + (int64_t)t.e * p.a_rows + i);
-        if (NA == 2) bias_b = __ldg(p.bias + (int64_t)t.e * p.a_rows + p.I + i);
-      }
+      const float bias = lane_bias<MODE, SW>(p, t, row);
       const bool ready = !*s_abort && ptx::mbar_wait_bounded(&accf[b2], (uint32_t)(li >> 1) & 1, s_abort, kWaitNs);
       // (one answer for all epilogue warps: another role may raise the abort flag at any time)
       if (ptx::bar_or<1, 32 * C::EPI_WARPS>(!ready)) break;
@@ -801,16 +881,15 @@ __global__ void __launch_bounds__(PairCfg<MODE, NA>::THREADS, 1)
       };
       if (32 * part >= t.nw) release();
       for (int c0 = 32 * part; c0 < t.nw; c0 += 64) {
-        uint32_t va[32], vb[32];
-        ptx::tmem_ld32(acc + c0, va);
-        if (NA == 2) ptx::tmem_ld32(acc + C::NB + c0, vb);
+        uint32_t v[32];
+        ptx::tmem_ld32(acc + c0, v);
         ptx::tmem_wait_ld();
         if (c0 + 64 >= t.nw) release();
         if (!have) {   // an expert without rows: the accumulator was never written
 #pragma unroll
-          for (int c = 0; c < 32; ++c) va[c] = vb[c] = 0u;
+          for (int c = 0; c < 32; ++c) v[c] = 0u;
         }
-        finish<MODE, NA>(p, t, va, vb, c0, i, bias_a, bias_b);
+        finish<MODE, SW, BF>(p, t, v, bias, c0, row, epi + kEpiBytes * part, 2 + part);
       }
     }
   }
@@ -922,12 +1001,12 @@ int64_t row_tiles_bound(const LinArgs& a, int nw) {
   return (a.rows - used) / nw + used;
 }
 
-template <int MODE, int NA, int NB>
-int launch_split(const LinArgs& a) {
-  using C = SplitCfg<MODE, NA, NB>;
+template <int MODE, bool SW, int NB, bool BF>
+int launch_split_of(const LinArgs& a) {
+  using C = SplitCfg<MODE, NB>;
   CUtensorMap ma, mb;
-  if (!operand_maps(a, 128, C::B_BOX, &ma, &mb)) return -1;
-  LinParams p = params_of(a, 128);
+  if (!operand_maps(a, SW ? 64 : 128, C::B_BOX, &ma, &mb)) return -1;
+  LinParams p = params_of(a, SW ? 64 : 128);
   p.nw_max = NB;
   p.n_jt = (a.N + NB - 1) / NB;
   const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, NB)) * p.n_it;
@@ -936,7 +1015,7 @@ int launch_split(const LinArgs& a) {
   const int64_t blocks = MODE == kWeightGrad ? (a.rows / (a.offsets ? a.E : 1) + kBK - 1) / kBK : (p.C + kBK - 1) / kBK;
   int64_t s = std::min<int64_t>((int64_t)multiprocessors() * C::CPS / tiles, blocks / 2);
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, 8));
-  auto kern = lin_split_kernel<MODE, NA, NB>;
+  auto kern = lin_split_kernel<MODE, SW, NB, BF>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, C::SMEM, done)) return -1;
   const int64_t grid = tiles * p.splits;
@@ -973,16 +1052,16 @@ int pair_slots(K kern, int threads, int smem, std::atomic<int>* known) {
   return n;
 }
 
-template <int MODE, int NA>
-int launch_pair(const LinArgs& a) {
-  using C = PairCfg<MODE, NA>;
+template <int MODE, bool SW, bool BF>
+int launch_pair_of(const LinArgs& a) {
+  using C = PairCfg<MODE>;
   CUtensorMap ma, mb;
-  if (!operand_maps(a, 128, 64, &ma, &mb)) return -1;
-  LinParams p = params_of(a, 256);
+  if (!operand_maps(a, SW ? 64 : 128, 64, &ma, &mb)) return -1;
+  LinParams p = params_of(a, SW ? 128 : 256);
   p.nw_max = C::NB;
   p.n_jt = (a.N + C::NB - 1) / C::NB;
   p.splits = 1;
-  auto kern = lin_pair_kernel<MODE, NA>;
+  auto kern = lin_pair_kernel<MODE, SW, BF>;
   static std::atomic<uint64_t> done{0};
   static std::atomic<int> slots[64];
   if (!allow_smem(kern, C::SMEM, done)) return -1;
@@ -994,9 +1073,19 @@ int launch_pair(const LinArgs& a) {
                  cudaSuccess ? 1 : -1;
 }
 
-// Tiles of 256 x nw that the product makes (on average over the experts' counts).
-int64_t pair_tiles(const LinArgs& a, int nw) {
-  const int64_t I = a.mode != kForward ? a.K : a.fn == MOE_FN_SWIGLU ? a.N / 2 : a.N;
+template <int MODE, bool SW = false>
+int launch_pair(const LinArgs& a) {
+  return a.bf16 ? launch_pair_of<MODE, SW, true>(a) : launch_pair_of<MODE, SW, false>(a);
+}
+template <int MODE, bool SW, int NB>
+int launch_split(const LinArgs& a) {
+  return a.bf16 ? launch_split_of<MODE, SW, NB, true>(a) : launch_split_of<MODE, SW, NB, false>(a);
+}
+
+// Tiles of 256 x 256 that the product makes (on average over the experts' counts).
+int64_t pair_tiles(const LinArgs& a) {
+  constexpr int nw = 256;
+  const int64_t I = a.mode == kForward ? a.N : a.K;
   const int64_t j = a.mode == kWeightGrad ? a.E * (int64_t)((a.N + nw - 1) / nw)
                     : a.offsets           ? std::min<int64_t>(a.E, a.rows) * ((a.rows / a.E + nw - 1) / nw)
                                           : (a.rows + nw - 1) / nw;
@@ -1007,21 +1096,20 @@ int64_t pair_tiles(const LinArgs& a, int nw) {
 
 int launch_linear(const LinArgs& a) {
   const bool narrow = a.rows <= 32 * (a.offsets ? a.E : 1);   // few rows an expert: the weights' stream is the work
-  const bool swiglu = a.mode == kForward && a.fn == MOE_FN_SWIGLU;
   // CTA pairs once their tiles fill about half of the SMs (fewer: smaller tiles on more SMs).
-  const bool pair = pair_tiles(a, swiglu ? 128 : 256) >= multiprocessors() / 4 && (a.mode == kWeightGrad || !narrow);
+  const bool pair = pair_tiles(a) >= multiprocessors() / 4 && (a.mode == kWeightGrad || !narrow);
   switch (a.mode) {
     case kForward:
-      if (swiglu)
-        return pair ? launch_pair<kForward, 2>(a) : narrow ? launch_split<kForward, 2, 32>(a)
-                                                           : launch_split<kForward, 2, 128>(a);
-      return pair ? launch_pair<kForward, 1>(a) : narrow ? launch_split<kForward, 1, 32>(a)
-                                                         : launch_split<kForward, 1, 128>(a);
+      if (a.fn == MOE_FN_SWIGLU)
+        return pair ? launch_pair<kForward, true>(a) : narrow ? launch_split<kForward, true, 32>(a)
+                                                              : launch_split<kForward, true, 128>(a);
+      return pair ? launch_pair<kForward>(a) : narrow ? launch_split<kForward, false, 32>(a)
+                                                      : launch_split<kForward, false, 128>(a);
     case kInputGrad:
-      return pair ? launch_pair<kInputGrad, 1>(a) : narrow ? launch_split<kInputGrad, 1, 32>(a)
-                                                           : launch_split<kInputGrad, 1, 128>(a);
+      return pair ? launch_pair<kInputGrad>(a) : narrow ? launch_split<kInputGrad, false, 32>(a)
+                                                        : launch_split<kInputGrad, false, 128>(a);
     default:
-      return pair ? launch_pair<kWeightGrad, 1>(a) : launch_split<kWeightGrad, 1, 128>(a);
+      return pair ? launch_pair<kWeightGrad>(a) : launch_split<kWeightGrad, false, 128>(a);
   }
 }
 
@@ -1032,6 +1120,9 @@ int launch_linear(const LinArgs& a) {
 // adds up per expert.  The sums take dz before its rounding to 16 bits.
 namespace {
 constexpr int kChunk = 64;
+
+__device__ __forceinline__ float from16r(uint16_t v, bool bf) { return bf ? from16<true>(v) : from16<false>(v); }
+__device__ __forceinline__ uint16_t to16r(float v, bool bf) { return bf ? to16<true>(v) : to16<false>(v); }
 
 struct ActGradParams {
   int32_t rows, N, No, E, bf16, fn, chunks;
@@ -1116,7 +1207,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
         const uint16_t* d16 = reinterpret_cast<const uint16_t*>(&dv);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float g0 = from16(g16[k], bf), u0 = from16(u16[k], bf), d = from16(d16[k], bf);
+          const float g0 = from16r(g16[k], bf), u0 = from16r(u16[k], bf), d = from16r(d16[k], bf);
           const float g = clamp_hi(g0, p.limit), u = clamp_both(u0, p.limit);
           const float s = __fdividef(1.f, 1.f + __expf(-g));
           if (col < p.No) o[k] = g0 > p.limit ? 0.f : d * u * s * (1.f + g * (1.f - s));
@@ -1129,13 +1220,13 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
         const uint16_t* z16 = reinterpret_cast<const uint16_t*>(&zv);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          o[k] = act_grad<FN>(FN != MOE_FN_NONE ? from16(z16[k], bf) : 0.f, from16(d16[k], bf));
+          o[k] = act_grad<FN>(FN != MOE_FN_NONE ? from16r(z16[k], bf) : 0.f, from16r(d16[k], bf));
       }
       if (FN != MOE_FN_NONE) {
         uint4 ov;
         uint16_t* o16 = reinterpret_cast<uint16_t*>(&ov);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o16[k] = to16(o[k], bf);
+        for (int k = 0; k < 8; ++k) o16[k] = to16r(o[k], bf);
         *reinterpret_cast<uint4*>(p.dz + (int64_t)r * p.N + col) = ov;
       }
 #pragma unroll
