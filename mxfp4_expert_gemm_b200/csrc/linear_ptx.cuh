@@ -72,11 +72,19 @@ __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* m
       : "memory");
 }
 
-// Load from the shared memory of a CTA of the cluster (cluster-window address).
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
+// Arrive on a barrier of another CTA of the cluster without waiting for this thread's earlier
+// stores (mbar_arrive_cluster releases them: a round trip to L2 while stores are in flight).
+// For handing back TMEM whose reads tcgen05.wait::ld has completed.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster_addr) : "memory");
+}
+
+// Copy from this CTA's shared memory to a cluster CTA's (cluster-window addresses of the
+// destination and of the barrier there that counts the bytes); size a multiple of 16.
+__device__ __forceinline__ void bulk_copy_cluster(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+               : "memory");
 }
 
 }  // namespace ptx

@@ -123,7 +123,7 @@ __device__ __forceinline__ int tile_width(int cnt, int nt, int step) {
 // per lane).  Tiles run expert by expert; within an expert, JFAST: its token tiles run
 // fastest (CTAs that start together then share a weight tile in L2), else its i tiles.
 template <bool JFAST>
-__device__ __forceinline__ LinTile find_row_tile(const LinParams& p, int64_t item, int step, int iw) {
+__device__ __forceinline__ LinTile find_row_tile(const LinParams& p, uint32_t item, int step, int iw) {
   const int lane = threadIdx.x & 31;
   LinTile t;
   t.ok = 0;
@@ -131,9 +131,9 @@ __device__ __forceinline__ LinTile find_row_tile(const LinParams& p, int64_t ite
   t.clen = p.C;
   if (!p.offsets) {
     const int nt = (p.rows + p.nw_max - 1) / p.nw_max, w = tile_width(p.rows, nt, step);
-    if (item < (int64_t)nt * p.n_it) {
-      const int jt = JFAST ? (int)(item % nt) : (int)(item / p.n_it);
-      const int it = JFAST ? (int)(item / nt) : (int)(item % p.n_it);
+    if (item < (uint32_t)nt * (uint32_t)p.n_it) {
+      const int jt = JFAST ? item % (uint32_t)nt : item / (uint32_t)p.n_it;
+      const int it = JFAST ? item / (uint32_t)nt : item % (uint32_t)p.n_it;
       t.ok = 1;
       t.e = 0;
       t.i0 = it * iw;
@@ -164,17 +164,17 @@ __device__ __forceinline__ LinTile find_row_tile(const LinParams& p, int64_t ite
     if (lane >= o) incl += v;
   }
   if (__any_sync(0xffffffffu, bad) && item == 0 && lane == 0) set_status(p.status, MOE_ERR_INVALID_ARG);
-  const int64_t lo = (int64_t)(incl - sum) * p.n_it, hi = (int64_t)incl * p.n_it;
+  const uint32_t lo = (uint32_t)(incl - sum) * p.n_it, hi = (uint32_t)incl * p.n_it;
   const unsigned who = __ballot_sync(0xffffffffu, item >= lo && item < hi);
   if (!who) return t;
   const int src = __ffs(who) - 1;
   int fe = 0, fa = 0, fc = 0, floc = 0;
   if (lane == src) {
-    int64_t base = lo;
+    uint32_t base = lo;
     bool found = false;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int64_t n = (int64_t)((cnt[k] + p.nw_max - 1) / p.nw_max) * p.n_it;
+      const uint32_t n = (uint32_t)((cnt[k] + p.nw_max - 1) / p.nw_max) * p.n_it;
       if (!found && item < base + n) {
         found = true;
         fe = 8 * lane + k;
@@ -201,13 +201,13 @@ __device__ __forceinline__ LinTile find_row_tile(const LinParams& p, int64_t ite
 }
 
 // Tile `item` of a weight gradient: every expert has the same tiles, its own contraction range.
-__device__ __forceinline__ LinTile find_weight_tile(const LinParams& p, int64_t item, int step, int iw) {
+__device__ __forceinline__ LinTile find_weight_tile(const LinParams& p, uint32_t item, int step, int iw) {
   LinTile t;
   const int per_e = p.n_it * p.n_jt;
-  t.ok = item < (int64_t)per_e * p.E;
+  t.ok = item < (uint32_t)per_e * (uint32_t)p.E;
   if (!t.ok) return t;
-  t.e = (int)(item / per_e);
-  const int loc = (int)(item - (int64_t)t.e * per_e);
+  t.e = item / (uint32_t)per_e;
+  const int loc = item - (uint32_t)t.e * per_e;
   const int w = tile_width(p.J, p.n_jt, step);
   t.i0 = (loc % p.n_it) * iw;
   t.j0 = (loc / p.n_it) * w;
@@ -226,14 +226,14 @@ __device__ __forceinline__ LinTile find_weight_tile(const LinParams& p, int64_t 
 }
 
 template <int MODE, bool JFAST>
-__device__ __forceinline__ LinTile find_tile(const LinParams& p, int64_t item, int step, int iw) {
+__device__ __forceinline__ LinTile find_tile(const LinParams& p, uint32_t item, int step, int iw) {
   if (MODE == kWeightGrad) return find_weight_tile(p, item, step, iw);
   return find_row_tile<JFAST>(p, item, step, iw);
 }
 
 // The experts' row ranges and tiles, kept in shared memory by kernels that take many tiles.
 struct RowTable {
-  int64_t items;
+  uint32_t items, pad;
   int32_t start[256], cnt[256];
   int32_t base[257];         // first tile (along j) of each expert
 };
@@ -273,19 +273,19 @@ __device__ __forceinline__ void build_table(const LinParams& p, RowTable* tab) {
   }
   if (lane == 31) {
     tab->base[256] = incl;
-    tab->items = (int64_t)incl * p.n_it;
+    tab->items = (uint32_t)incl * p.n_it;
   }
   if (__any_sync(0xffffffffu, bad) && lane == 0 && blockIdx.x == 0) set_status(p.status, MOE_ERR_INVALID_ARG);
 }
 
 // Tile `item` (< items) by the whole warp: expert by expert, tiles along i fastest.
 template <int MODE>
-__device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable* tab, int64_t item, int step, int iw) {
+__device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable* tab, uint32_t item, int step, int iw) {
   const int lane = threadIdx.x & 31;
-  const int q = (int)(item / p.n_it);
+  const int q = item / (uint32_t)p.n_it;
   LinTile t;
   t.ok = 1;
-  t.i0 = (int)(item - (int64_t)q * p.n_it) * iw;
+  t.i0 = (int)(item - (uint32_t)q * p.n_it) * iw;
   t.e = 0;
   if (p.E > 1) {   // the lane, then the expert of its eight, whose tiles hold q
     const unsigned m = __ballot_sync(0xffffffffu, tab->base[8 * lane] <= q && q < tab->base[8 * lane + 8]);
@@ -474,6 +474,16 @@ __device__ __forceinline__ float lane_bias(const LinParams& p, const LinTile& t,
   return i < p.I ? __ldg(p.bias + (int64_t)t.e * p.a_rows + (SW && row >= 64 ? p.I : 0) + i) : 0.f;
 }
 
+// 32 accumulator columns of this warp's lanes (zeros where no contraction block was added).
+__device__ __forceinline__ void load_acc(uint32_t taddr, bool have, uint32_t (&v)[32]) {
+  ptx::tmem_ld32(taddr, v);
+  ptx::tmem_wait_ld();
+  if (!have) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = 0u;
+  }
+}
+
 // ------------------------------------------------------------------------------ split kernel
 // One CTA (or a cluster of `splits` CTAs that share a tile's contraction) per output tile of
 // 128 i x at most NB j (SwiGLU: 64 gate and the matching 64 up features).
@@ -487,12 +497,15 @@ struct SplitCfg {
   static constexpr int CPS = 2;                         // CTAs per SM
   static constexpr int S = 108 * 1024 / STAGE;
   static constexpr int TMEM_COLS = NB;
-  static constexpr int RED_BYTES = NB * 128 * 4;        // fp32 partial tile, and the epilogue's
-  static constexpr int EPI_OFF = RED_BYTES;             // buffer: both reuse the stages
-  static constexpr int BAR_BYTES = 8 * (2 * S + 2) + 64;
+  // The stages are reused: the tile's fp32 partials, the received ones ([splits][ceil(nw /
+  // splits)][128]), the epilogue's buffer.  128-wide tiles leave no room for the first two.
+  static constexpr bool SPLIT = NB <= 64;
+  static constexpr int SEND_BYTES = SPLIT ? NB * 512 : 0, RED_BYTES = SPLIT ? (NB + 8) * 512 : 0;
+  static constexpr int EPI_OFF = SEND_BYTES + RED_BYTES;
+  static constexpr int BAR_BYTES = 8 * (2 * S + 3) + 64;
   static constexpr int SMEM = S * STAGE + BAR_BYTES + 1024 /* align slack */;
   static constexpr int THREADS = 32 * 6;                // producer, MMA, four epilogue warps
-  static_assert(RED_BYTES + kEpiBytes <= S * STAGE, "the partial tile and the epilogue's buffer fit the stages");
+  static_assert(EPI_OFF + kEpiBytes <= S * STAGE, "the partial tile and the epilogue's buffer fit the stages");
   static_assert((SMEM + 1024) * CPS <= 228 * 1024, "shared memory of the co-resident CTAs");
   static_assert((NB == 32 || NB == 64 || NB == 128) && (!B_MN || NB % 64 == 0), "tile width");
 };
@@ -508,14 +521,16 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
   uint64_t* sfree = full + C::S;
   uint64_t* accf = sfree + C::S;
   uint64_t* drain = accf + 1;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* redf = drain + 1;        // the peers' partials have arrived
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(redf + 1);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   LinTile* s_tile = reinterpret_cast<LinTile*>(s_tmem + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int S = p.splits;
+  constexpr bool SPLIT = C::SPLIT;
+  const int S = SPLIT ? p.splits : 1;
   const int rank = S > 1 ? (int)ptx::cluster_ctarank() : 0;
-  const int64_t item = blockIdx.x / S;
+  const uint32_t item = blockIdx.x / (unsigned)S;
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < C::S; ++s) {
@@ -524,6 +539,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
     }
     ptx::mbar_init(accf, 1);
     ptx::mbar_init(drain, 1);
+    ptx::mbar_init(redf, 1);
     *s_abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&tm_a);
@@ -634,20 +650,11 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
     if (!ptx::bar_or<1, 128>(!ready) && t.ok) {
       ptx::tc_fence_after();
       const float bias = lane_bias<MODE, SW>(p, t, row);
-      float* red = reinterpret_cast<float*>(smem);
-      for (int c0 = 0; c0 < t.nw; c0 += 32) {
-        uint32_t v[32];
-        ptx::tmem_ld32(acc + c0, v);
-        ptx::tmem_wait_ld();
-        if (!have) {   // no contraction block here: the accumulator was never written
-#pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = 0u;
-        }
-        if (S == 1) {
+      if (S == 1) {
+        for (int c0 = 0; c0 < t.nw; c0 += 32) {
+          uint32_t v[32];
+          load_acc(acc + c0, have, v);
           finish<MODE, SW, BF>(p, t, v, bias, c0, row, smem + C::EPI_OFF, 2);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) red[(c0 + c) * 128 + row] = __uint_as_float(v[c]);
         }
       }
     }
@@ -655,34 +662,63 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
 
   __syncthreads();
   if (*s_abort && threadIdx.x == 0) set_status(p.status, MOE_ERR_TIMEOUT);
-  if (S > 1) {
-    // The cluster's partial tiles meet over distributed shared memory: CTA r adds and finishes
-    // its share of the columns, in rank order, so that the sum does not depend on timing.  A
-    // rank's 32 loads per thread are issued together (one after another they took 40 us).
-    ptx::cluster_sync();
+  if (SPLIT && S > 1) {
+    // The cluster's partial tiles meet over distributed shared memory: CTA r finishes its share
+    // of the columns, whose partials every CTA sends it by one bulk copy (loads or stores by the
+    // threads took up to 30 us here).  The sum runs in rank order, so that it does not depend
+    // on timing.
+    const int row = 32 * (warp & 3) + lane;
+    const int per = (t.nw + S - 1) / S;   // columns per CTA
+    auto share = [&](int r) { return max(0, min((r + 1) * per, t.nj) - r * per); };   // valid columns of CTA r
+    float* src = reinterpret_cast<float*>(smem);                       // [nw][128]
+    float* dst = reinterpret_cast<float*>(smem + C::SEND_BYTES);       // [S][per][128]
     if (warp >= 2 && t.ok) {
-      const int row = 32 * (warp & 3) + lane;
-      const float bias = lane_bias<MODE, SW>(p, t, row);
-      const int per = (t.nw + S - 1) / S;   // columns per CTA
-      const int c1 = min((rank + 1) * per, t.nj);
-      LinTile mine = t;
-      mine.nj = c1;
-      for (int c0 = rank * per; c0 < c1; c0 += 32) {
+      const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+      for (int c0 = 0; c0 < t.nj; c0 += 32) {
         uint32_t v[32];
+        load_acc(acc + c0, kb1 > kb0, v);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] = 0u;
+        for (int c = 0; c < 32; ++c) src[(c0 + c) * 128 + row] = __uint_as_float(v[c]);
+      }
+      ptx::fence_proxy_async_smem();   // the copies read what the threads wrote
+    }
+    if (threadIdx.x == 0 && t.ok) ptx::mbar_arrive_expect_tx(redf, (uint32_t)(S * share(rank) * 512));
+    ptx::cluster_sync();   // every CTA is done with its stages and expects its copies
+    if (warp == 0 && t.ok) {
+      if (ptx::elect_one()) {
         for (int r = 0; r < S; ++r) {
-          const uint32_t peer = ptx::mapa_shared(smem + (c0 * 128 + row) * 4, r);
-          float w[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) w[c] = c0 + c < c1 ? ptx::ld_cluster_f32(peer + c * 512) : 0.f;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) + w[c]);
+          const int n = share(r);
+          if (n > 0)
+            ptx::bulk_copy_cluster(ptx::mapa_shared(dst + rank * per * 128, r), src + r * per * 128, (uint32_t)n * 512,
+                                   ptx::mapa_shared(redf, r));
         }
-        finish<MODE, SW, BF>(p, mine, v, bias, c0, row, smem + C::EPI_OFF, 2);
+      }
+      __syncwarp();
+    }
+    if (warp >= 2 && t.ok) {
+      const bool here = ptx::mbar_wait_cluster_bounded(redf, 0, s_abort, kWaitNs);
+      if (!ptx::bar_or<1, 128>(!here)) {
+        const float bias = lane_bias<MODE, SW>(p, t, row);
+        const int c1 = min((rank + 1) * per, t.nj);
+        LinTile part = t;
+        part.nj = c1;
+        const float* red = dst + row;
+        for (int c0 = rank * per; c0 < c1; c0 += 32) {
+          uint32_t v[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            float sum = 0.f;
+            if (c0 + c < c1)
+              for (int r = 0; r < S; ++r) sum += red[(r * per + c0 + c - rank * per) * 128];
+            v[c] = __float_as_uint(sum);
+          }
+          finish<MODE, SW, BF>(p, part, v, bias, c0, row, smem + C::EPI_OFF, 2);
+        }
+      } else {
+        set_status(p.status, MOE_ERR_TIMEOUT);
       }
     }
-    ptx::cluster_sync();   // no CTA leaves while a peer reads its partial tile
+    ptx::cluster_sync();   // no CTA leaves while its copies are under way
   }
   if (warp == 1) {
     ptx::tc_fence_after();
@@ -731,7 +767,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   constexpr int kIW = SW ? 128 : 256;   // columns of out per tile
   const int rank = (int)ptx::cluster_ctarank();
-  const int unit0 = blockIdx.x / 2, units = gridDim.x / 2;
+  const uint32_t unit0 = blockIdx.x / 2, units = gridDim.x / 2;
 
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < C::S; ++s) {
@@ -757,13 +793,13 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
   ptx::cluster_sync();   // the peer's copies, commits and arrivals find initialized barriers
   ptx::tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int64_t n_items = tab->items;
+  const uint32_t n_items = tab->items;
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer (each CTA its share)
     int64_t g = 0;
     bool stop = false, withheld = false;
-    for (int64_t item = unit0; item < n_items && !stop; item += units) {
+    for (uint32_t item = unit0; item < n_items && !stop; item += units) {
       const LinTile t = table_tile<MODE>(p, tab, item, 32, kIW);
       const int kb_all = (t.clen + kBK - 1) / kBK, half = t.nw / 2, nbox = (half + 63) / 64;
       for (int kb = 0; kb < kb_all; ++kb, ++g) {
@@ -821,7 +857,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       int64_t g = 0;
       int li = 0;
       bool stop = false;
-      for (int64_t item = unit0; item < n_items && !stop; item += units, ++li) {
+      for (uint32_t item = unit0; item < n_items && !stop; item += units, ++li) {
         const LinTile t = table_tile<MODE>(p, tab, item, 32, kIW);
         const int kb_all = (t.clen + kBK - 1) / kBK, b2 = li & 1;
         const uint32_t idesc = ptx::idesc_f16(BF, 256, t.nw, C::A_MN, C::B_MN);
@@ -863,7 +899,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     // ---------------------------------------------------------------- epilogue warps
     const int q = warp & 3, row = 32 * q + lane, part = (warp - 2) >> 2;
     int li = 0;
-    for (int64_t item = unit0; item < n_items; item += units, ++li) {
+    for (uint32_t item = unit0; item < n_items; item += units, ++li) {
       LinTile t = table_tile<MODE>(p, tab, item, 32, kIW);
       t.i0 += kIW / 2 * rank;
       const int b2 = li & 1;
@@ -877,7 +913,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       auto release = [&] {   // this warp's reads are done: one arrival on the leader's barrier
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(&acce[b2], 0));
+        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(&acce[b2], 0));
       };
       if (32 * part >= t.nw) release();
       for (int c0 = 32 * part; c0 < t.nw; c0 += 64) {
@@ -1014,7 +1050,7 @@ int launch_split_of(const LinArgs& a) {
   // keeping at least two 64-wide blocks of it.
   const int64_t blocks = MODE == kWeightGrad ? (a.rows / (a.offsets ? a.E : 1) + kBK - 1) / kBK : (p.C + kBK - 1) / kBK;
   int64_t s = std::min<int64_t>((int64_t)multiprocessors() * C::CPS / tiles, blocks / 2);
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, 8));
+  p.splits = C::SPLIT ? (int)std::max<int64_t>(1, std::min<int64_t>(s, 8)) : 1;
   auto kern = lin_split_kernel<MODE, SW, NB, BF>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, C::SMEM, done)) return -1;
@@ -1095,21 +1131,33 @@ int64_t pair_tiles(const LinArgs& a) {
 }  // namespace
 
 int launch_linear(const LinArgs& a) {
-  const bool narrow = a.rows <= 32 * (a.offsets ? a.E : 1);   // few rows an expert: the weights' stream is the work
+  const int64_t per = a.rows / (a.offsets ? a.E : 1);   // rows an expert, on average
+  const bool narrow = per <= 32;                        // the weights' stream is the work
+  const bool swiglu = a.mode == kForward && a.fn == MOE_FN_SWIGLU;
   // CTA pairs once their tiles fill about half of the SMs (fewer: smaller tiles on more SMs).
   const bool pair = pair_tiles(a) >= multiprocessors() / 4 && (a.mode == kWeightGrad || !narrow);
+  // 128-wide tiles once they alone fill the SMs, else 64-wide ones whose contraction clusters share.
+  const bool wide = 4 * pair_tiles(a) >= multiprocessors();
   switch (a.mode) {
     case kForward:
-      if (a.fn == MOE_FN_SWIGLU)
-        return pair ? launch_pair<kForward, true>(a) : narrow ? launch_split<kForward, true, 32>(a)
-                                                              : launch_split<kForward, true, 128>(a);
-      return pair ? launch_pair<kForward>(a) : narrow ? launch_split<kForward, false, 32>(a)
-                                                      : launch_split<kForward, false, 128>(a);
+      if (swiglu)
+        return pair     ? launch_pair<kForward, true>(a)
+               : narrow ? launch_split<kForward, true, 32>(a)
+               : wide   ? launch_split<kForward, true, 128>(a)
+                        : launch_split<kForward, true, 64>(a);
+      return pair     ? launch_pair<kForward>(a)
+             : narrow ? launch_split<kForward, false, 32>(a)
+             : wide   ? launch_split<kForward, false, 128>(a)
+                      : launch_split<kForward, false, 64>(a);
     case kInputGrad:
-      return pair ? launch_pair<kInputGrad>(a) : narrow ? launch_split<kInputGrad, false, 32>(a)
-                                                        : launch_split<kInputGrad, false, 128>(a);
+      return pair     ? launch_pair<kInputGrad>(a)
+             : narrow ? launch_split<kInputGrad, false, 32>(a)
+             : wide   ? launch_split<kInputGrad, false, 128>(a)
+                      : launch_split<kInputGrad, false, 64>(a);
     default:
-      return pair ? launch_pair<kWeightGrad>(a) : launch_split<kWeightGrad, false, 128>(a);
+      return pair ? launch_pair<kWeightGrad>(a)
+             : wide ? launch_split<kWeightGrad, false, 128>(a)
+                    : launch_split<kWeightGrad, false, 64>(a);
   }
 }
 
