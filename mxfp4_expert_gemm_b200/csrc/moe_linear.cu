@@ -581,9 +581,8 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
         ptx::mbar_arrive_expect_tx(&full[s], C::A_PANEL + nbox * C::B_BOX * 128);
         const int c = kb * kBK;
         if (MODE == kForward) {
-          const int arow = t.e * p.a_rows + t.i0;
-          ptx::tma_load_2d(a, &tm_a, c, arow, &full[s]);
-          if (SW) ptx::tma_load_2d(a + 8192, &tm_a, c, arow + p.I, &full[s]);   // (boxes of 64 rows)
+          if (SW) ptx::tma_load_3d(a, &tm_a, c, t.i0, 2 * t.e, &full[s]);
+          else ptx::tma_load_2d(a, &tm_a, c, t.e * p.a_rows + t.i0, &full[s]);
         } else if (MODE == kInputGrad) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) ptx::tma_load_3d(a + h * 8192, &tm_a, t.i0 + 64 * h, c, t.e, &full[s]);
@@ -740,8 +739,10 @@ struct PairCfg {
   static constexpr int B_BYTES = NB / 2 * 128;          // this CTA's half of B
   static constexpr int STAGE = A_PANEL + B_BYTES;
   static constexpr int S = 6;
+  static constexpr int STEP = 32;                       // tile widths along j: two halves of 16 rows
   static constexpr int EPI_WARPS = 8;
-  static constexpr int THREADS = 32 * (2 + EPI_WARPS);
+  static constexpr int B_WARP = 2 + EPI_WARPS;          // A's copies, MMA, epilogue, B's copies
+  static constexpr int THREADS = 32 * (3 + EPI_WARPS);
   static constexpr int BAR_BYTES = 8 * (2 * S + 5) + 16;
   static constexpr int SMEM = S * STAGE + 2 * kEpiBytes + BAR_BYTES + (int)sizeof(RowTable) + 1024 /* align slack */;
   static_assert(SMEM <= 227 * 1024 && S >= 4, "shared memory of one CTA per SM");
@@ -750,7 +751,7 @@ struct PairCfg {
 template <int MODE, bool SW, bool BF>
 __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                    const LinParams p) {
+                    const __grid_constant__ CUtensorMap tm_b64, const LinParams p) {
   using C = PairCfg<MODE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -783,6 +784,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&tm_a);
     ptx::prefetch_tensormap(&tm_b);
+    ptx::prefetch_tensormap(&tm_b64);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(s_tmem, 512);
@@ -795,15 +797,21 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
   const uint32_t tmem = *s_tmem;
   const uint32_t n_items = tab->items;
 
-  if (warp == 0) {
-    // ---------------------------------------------------------------- producer (each CTA its share)
-    int64_t g = 0;
+  if (warp == 0 || warp == C::B_WARP) {
+    // ---------------------------------------------------------------- producers (each CTA its share)
+    // One warp copies A, another B: a stage's copies are then issued side by side, each operand
+    // by as few copies as its layout allows (B in boxes of 64 rows instead of 128: 8% slower).
+    const bool is_a = warp == 0;
+    int g = 0;
     bool stop = false, withheld = false;
     for (uint32_t item = unit0; item < n_items && !stop; item += units) {
-      const LinTile t = table_tile<MODE>(p, tab, item, 32, kIW);
-      const int kb_all = (t.clen + kBK - 1) / kBK, half = t.nw / 2, nbox = (half + 63) / 64;
+      const LinTile t = table_tile<MODE>(p, tab, item, C::STEP, kIW);
+      const int kb_all = (t.clen + kBK - 1) / kBK, half = t.nw / 2;
+      const bool narrow = half <= 64;   // B of one 64-row box
+      const uint32_t bytes = 2 * (C::A_PANEL + (narrow ? 8192 : 16384));
+      const int i0 = t.i0 + kIW / 2 * rank, j0 = t.j0 + half * rank;
       for (int kb = 0; kb < kb_all; ++kb, ++g) {
-        const int s = (int)(g % C::S);
+        const int s = g % C::S;
         bool ok = true;
         if (g >= C::S) ok = ptx::mbar_wait_bounded(&sfree[s], (uint32_t)(g / C::S - 1) & 1, s_abort, kWaitNs);
         if (!__all_sync(0xffffffffu, ok)) {
@@ -818,23 +826,26 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
           uint8_t* a = smem + s * C::STAGE;
           uint8_t* b = a + C::A_PANEL;
           const uint32_t bar = ptx::mapa_shared(&full[s], 0);
-          if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * (C::A_PANEL + nbox * 8192));
-          const int c = kb * kBK, i0 = t.i0 + kIW / 2 * rank, j0 = t.j0 + half * rank;
-          if (MODE == kForward) {
-            const int arow = t.e * p.a_rows + i0;
-            ptx::tma_load_2d_pair(a, &tm_a, c, arow, bar);
-            if (SW) ptx::tma_load_2d_pair(a + 8192, &tm_a, c, arow + p.I, bar);   // (boxes of 64 rows)
-          } else if (MODE == kInputGrad) {
+          const int c = kb * kBK;
+          const int d1 = tail_shift(t.clen - c), d2 = t.c0 + c;   // (kWeightGrad)
+          if (is_a) {
+            if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], bytes);
+            if (MODE == kForward) {
+              if (SW) ptx::tma_load_3d_pair(a, &tm_a, c, i0, 2 * t.e, bar);
+              else ptx::tma_load_2d_pair(a, &tm_a, c, t.e * p.a_rows + i0, bar);
+            } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) ptx::tma_load_3d_pair(a + h * 8192, &tm_a, i0 + 64 * h, c, t.e, bar);
-          }
-          if (MODE == kWeightGrad) {
-            const int d1 = tail_shift(t.clen - c), d2 = t.c0 + c;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) ptx::tma_load_3d_pair(a + h * 8192, &tm_a, i0 + 64 * h, d1, d2, bar);
-            for (int h = 0; h < nbox; ++h) ptx::tma_load_3d_pair(b + h * 8192, &tm_b, j0 + 64 * h, d1, d2, bar);
+              for (int h = 0; h < 2; ++h) {
+                if (MODE == kInputGrad) ptx::tma_load_3d_pair(a + h * 8192, &tm_a, i0 + 64 * h, c, t.e, bar);
+                else ptx::tma_load_3d_pair(a + h * 8192, &tm_a, i0 + 64 * h, d1, d2, bar);
+              }
+            }
+          } else if (MODE == kWeightGrad) {
+            ptx::tma_load_3d_pair(b, &tm_b, j0, d1, d2, bar);
+            if (!narrow) ptx::tma_load_3d_pair(b + 8192, &tm_b, j0 + 64, d1, d2, bar);
           } else {
-            for (int h = 0; h < nbox; ++h) ptx::tma_load_2d_pair(b + h * 8192, &tm_b, c, j0 + 64 * h, bar);
+            if (narrow) ptx::tma_load_2d_pair(b, &tm_b64, c, j0, bar);
+            else ptx::tma_load_2d_pair(b, &tm_b, c, j0, bar);
           }
         }
         __syncwarp();
@@ -844,7 +855,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     // of every slot, and the cluster barrier at the end holds the peer until it has
     if (rank == 0) {
       volatile int local_abort = 0;
-      for (int64_t q = (g > C::S ? g - C::S : 0); q < g; ++q) {
+      for (int q = (g > C::S ? g - C::S : 0); q < g; ++q) {
         if (withheld && q == 0) continue;
         ptx::mbar_wait_bounded(&full[q % C::S], (uint32_t)(q / C::S) & 1, &local_abort, kWaitNs);
       }
@@ -854,11 +865,11 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     // ---------------------------------------------------------------- MMA issuer (the leader's)
     if (rank == 0) {
       constexpr uint64_t kStepA = C::A_MN ? 2048 >> 4 : 32 >> 4, kStepB = C::B_MN ? 2048 >> 4 : 32 >> 4;
-      int64_t g = 0;
+      int g = 0;
       int li = 0;
       bool stop = false;
       for (uint32_t item = unit0; item < n_items && !stop; item += units, ++li) {
-        const LinTile t = table_tile<MODE>(p, tab, item, 32, kIW);
+        const LinTile t = table_tile<MODE>(p, tab, item, C::STEP, kIW);
         const int kb_all = (t.clen + kBK - 1) / kBK, b2 = li & 1;
         const uint32_t idesc = ptx::idesc_f16(BF, 256, t.nw, C::A_MN, C::B_MN);
         if (li >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait_cluster_bounded(
@@ -867,7 +878,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
         ptx::tc_fence_after();
         const uint32_t d = tmem + b2 * 256;
         for (int kb = 0; kb < kb_all; ++kb, ++g) {
-          const int s = (int)(g % C::S);
+          const int s = g % C::S;
           if (!__all_sync(0xffffffffu,
                           ptx::mbar_wait_bounded(&full[s], (uint32_t)(g / C::S) & 1, s_abort, kWaitNs))) {
             stop = true;
@@ -900,7 +911,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     const int q = warp & 3, row = 32 * q + lane, part = (warp - 2) >> 2;
     int li = 0;
     for (uint32_t item = unit0; item < n_items; item += units, ++li) {
-      LinTile t = table_tile<MODE>(p, tab, item, 32, kIW);
+      LinTile t = table_tile<MODE>(p, tab, item, C::STEP, kIW);
       t.i0 += kIW / 2 * rank;
       const int b2 = li & 1;
       const bool have = t.clen > 0;
@@ -959,34 +970,43 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Map of 16-bit values, 128-byte swizzle, boxes of 64 values x box1 x 1; strides in values.
+// Map of 16-bit values, 128-byte swizzle, boxes of 64 values x box1 x box2; strides in values.
 bool map16(CUtensorMap* m, bool bf16, const void* base, int rank, uint64_t d0, uint64_t d1, uint64_t s1, uint64_t d2,
-           uint64_t s2, uint32_t box1) {
+           uint64_t s2, uint32_t box1, uint32_t box2 = 1) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {d0, d1, d2}, strides[2] = {2 * s1, 2 * s2};
-  const cuuint32_t box[3] = {64, box1, 1}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, box1, box2}, es[3] = {1, 1, 1};
   return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, (cuuint32_t)rank,
             const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The operand maps of a product: a_box / b_box rows per copy of the K-major ones.
-bool operand_maps(const LinArgs& a, uint32_t a_box, uint32_t b_box, CUtensorMap* ma, CUtensorMap* mb) {
+// The map of A: 128 rows per copy of a K-major one (SwiGLU: 64 gate and the 64 matching up
+// rows), 64 x 64 boxes of an MN-major one.
+bool a_map(const LinArgs& a, CUtensorMap* m) {
   const bool bf = a.bf16 != 0;
   const uint64_t K = a.K, N = a.N, E = a.E, rows = a.rows;
   switch (a.mode) {
-    case kForward:   // W [E * N][K], x [rows][K]
-      return map16(ma, bf, a.other, 2, K, E * N, K, 1, 0, a_box) &&
-             map16(mb, bf, a.tok, 2, K, rows, a.ld_tok, 1, 0, b_box);
-    case kInputGrad: // W [E][N][K] (rows past an expert's N read zeros), dz [rows][N]
-      return map16(ma, bf, a.other, 3, K, N, K, E, N * K, 64) &&
-             map16(mb, bf, a.tok, 2, N, rows, a.ld_tok, 1, 0, b_box);
-    default:         // x, dz as [rows][64][values]: see tail_shift
-      return map16(ma, bf, a.other, 3, K, 64, a.ld_other, rows, a.ld_other, 64) &&
-             map16(mb, bf, a.tok, 3, N, 64, a.ld_tok, rows, a.ld_tok, 64);
+    case kForward:
+      if (a.fn == MOE_FN_SWIGLU)   // W [E * 2][N / 2][K]
+        return map16(m, bf, a.other, 3, K, N / 2, K, 2 * E, N / 2 * K, 64, 2);
+      return map16(m, bf, a.other, 2, K, E * N, K, 1, 0, 128);   // W [E * N][K]
+    case kInputGrad:   // W [E][N][K] (rows past an expert's N read zeros)
+      return map16(m, bf, a.other, 3, K, N, K, E, N * K, 64);
+    default:           // x as [rows][64][K]: see tail_shift
+      return map16(m, bf, a.other, 3, K, 64, a.ld_other, rows, a.ld_other, 64);
   }
+}
+
+// The map of B, `box` rows per copy of a K-major one.
+bool b_map(const LinArgs& a, uint32_t box, CUtensorMap* m) {
+  const bool bf = a.bf16 != 0;
+  const uint64_t rows = a.rows;
+  if (a.mode == kWeightGrad)   // dz as [rows][64][N]
+    return map16(m, bf, a.tok, 3, (uint64_t)a.N, 64, a.ld_tok, rows, a.ld_tok, 64);
+  return map16(m, bf, a.tok, 2, (uint64_t)(a.mode == kForward ? a.K : a.N), rows, a.ld_tok, 1, 0, box);
 }
 
 // Kernels' dynamic shared memory limit, set once per device.
@@ -1041,7 +1061,7 @@ template <int MODE, bool SW, int NB, bool BF>
 int launch_split_of(const LinArgs& a) {
   using C = SplitCfg<MODE, NB>;
   CUtensorMap ma, mb;
-  if (!operand_maps(a, SW ? 64 : 128, C::B_BOX, &ma, &mb)) return -1;
+  if (!a_map(a, &ma) || !b_map(a, C::B_BOX, &mb)) return -1;
   LinParams p = params_of(a, SW ? 64 : 128);
   p.nw_max = NB;
   p.n_jt = (a.N + NB - 1) / NB;
@@ -1091,8 +1111,8 @@ int pair_slots(K kern, int threads, int smem, std::atomic<int>* known) {
 template <int MODE, bool SW, bool BF>
 int launch_pair_of(const LinArgs& a) {
   using C = PairCfg<MODE>;
-  CUtensorMap ma, mb;
-  if (!operand_maps(a, SW ? 64 : 128, 64, &ma, &mb)) return -1;
+  CUtensorMap ma, mb, mb64;
+  if (!a_map(a, &ma) || !b_map(a, 128, &mb) || !b_map(a, 64, &mb64)) return -1;
   LinParams p = params_of(a, SW ? 128 : 256);
   p.nw_max = C::NB;
   p.n_jt = (a.N + C::NB - 1) / C::NB;
@@ -1105,7 +1125,7 @@ int launch_pair_of(const LinArgs& a) {
   if (n <= 0) return -1;
   const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, C::NB)) * p.n_it;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, n);
-  return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, false, 2u, ma, mb, p) ==
+  return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, false, 2u, ma, mb, mb64, p) ==
                  cudaSuccess ? 1 : -1;
 }
 
