@@ -731,6 +731,11 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
 // holds its 128 rows of A and half of B's rows, so a pair moves half the bytes into shared memory
 // per multiply-add that two single CTAs would.  The
 // accumulator is double-buffered in TMEM: the epilogue of a tile runs under the next tile's MMAs.
+// B's maps with boxes of 32, 64, 96 and 128 rows (kWeightGrad: one map).
+struct BMaps {
+  CUtensorMap m[4];
+};
+
 template <int MODE>
 struct PairCfg {
   static constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeightGrad;
@@ -750,8 +755,7 @@ struct PairCfg {
 
 template <int MODE, bool SW, bool BF>
 __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
-    lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                    const __grid_constant__ CUtensorMap tm_b64, const LinParams p) {
+    lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ BMaps tm_b, const LinParams p) {
   using C = PairCfg<MODE>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -783,8 +787,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     *s_abort = 0;
     ptx::fence_mbar_init();
     ptx::prefetch_tensormap(&tm_a);
-    ptx::prefetch_tensormap(&tm_b);
-    ptx::prefetch_tensormap(&tm_b64);
+    for (int m = 0; m < (MODE == kWeightGrad ? 1 : 4); ++m) ptx::prefetch_tensormap(&tm_b.m[m]);
   }
   if (warp == 1) {
     ptx::tmem_alloc_pair(s_tmem, 512);
@@ -807,8 +810,10 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     for (uint32_t item = unit0; item < n_items && !stop; item += units) {
       const LinTile t = table_tile<MODE>(p, tab, item, C::STEP, kIW);
       const int kb_all = (t.clen + kBK - 1) / kBK, half = t.nw / 2;
-      const bool narrow = half <= 64;   // B of one 64-row box
-      const uint32_t bytes = 2 * (C::A_PANEL + (narrow ? 8192 : 16384));
+      const int boxes = (half + 31) / 32;   // B's rows in units of 32, as one copy
+      const bool narrow = half <= 64;       // (kWeightGrad: one or two 64-wide copies)
+      const uint32_t bytes = 2 * (C::A_PANEL + (MODE != kWeightGrad ? 4096 * boxes : narrow ? 8192 : 16384));
+      const CUtensorMap* map_b = &tm_b.m[MODE == kWeightGrad ? 0 : boxes - 1];
       const int i0 = t.i0 + kIW / 2 * rank, j0 = t.j0 + half * rank;
       for (int kb = 0; kb < kb_all; ++kb, ++g) {
         const int s = g % C::S;
@@ -841,11 +846,10 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
               }
             }
           } else if (MODE == kWeightGrad) {
-            ptx::tma_load_3d_pair(b, &tm_b, j0, d1, d2, bar);
-            if (!narrow) ptx::tma_load_3d_pair(b + 8192, &tm_b, j0 + 64, d1, d2, bar);
+            ptx::tma_load_3d_pair(b, map_b, j0, d1, d2, bar);
+            if (!narrow) ptx::tma_load_3d_pair(b + 8192, map_b, j0 + 64, d1, d2, bar);
           } else {
-            if (narrow) ptx::tma_load_2d_pair(b, &tm_b64, c, j0, bar);
-            else ptx::tma_load_2d_pair(b, &tm_b, c, j0, bar);
+            ptx::tma_load_2d_pair(b, map_b, c, j0, bar);
           }
         }
         __syncwarp();
@@ -1111,8 +1115,11 @@ int pair_slots(K kern, int threads, int smem, std::atomic<int>* known) {
 template <int MODE, bool SW, bool BF>
 int launch_pair_of(const LinArgs& a) {
   using C = PairCfg<MODE>;
-  CUtensorMap ma, mb, mb64;
-  if (!a_map(a, &ma) || !b_map(a, 128, &mb) || !b_map(a, 64, &mb64)) return -1;
+  CUtensorMap ma;
+  BMaps mb;
+  if (!a_map(a, &ma)) return -1;
+  for (uint32_t m = 0; m < (MODE == kWeightGrad ? 1 : 4); ++m)
+    if (!b_map(a, 32 * (m + 1), &mb.m[m])) return -1;
   LinParams p = params_of(a, SW ? 128 : 256);
   p.nw_max = C::NB;
   p.n_jt = (a.N + C::NB - 1) / C::NB;
@@ -1125,7 +1132,7 @@ int launch_pair_of(const LinArgs& a) {
   if (n <= 0) return -1;
   const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, C::NB)) * p.n_it;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, n);
-  return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, false, 2u, ma, mb, mb64, p) ==
+  return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, false, 2u, ma, mb, p) ==
                  cudaSuccess ? 1 : -1;
 }
 
