@@ -414,7 +414,7 @@ moe_status moe_norm(int32_t kind, int32_t dtype, int32_t T, int32_t d, const voi
 
 /* Backward pass of moe_norm, from its x, w and statistics:  xh = (x - mean) * rstd,
  *   g = dy * w,  dx = rstd * (g - xh * mean(g * xh) - [LAYER] mean(g)) [+ dres],
- *   dw = sum over rows of dy * xh,  db = sum over rows of dy   (fp32 [d], NULL to skip)
+ *   dw = sum over rows of dy * xh,  [LAYER] db = sum over rows of dy   (fp32 [d], NULL to skip)
  * dres [T][d]: an optional gradient added to dx in the same pass (the residual stream's).  dx
  * may be dy, x or dres itself (same stride).  ws: moe_norm_workspace_bytes(T, d) bytes, needed
  * with dw or db.  T = 0 writes zeros to dw and db.  Errors: as moe_norm, MOE_ERR_WORKSPACE. */

@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <algorithm>
+#include <type_traits>
 
 #include "moe_linear.cuh"
 
@@ -43,26 +44,89 @@ __device__ __forceinline__ void store_pack(void* base, int64_t at, const Pack<DT
   *reinterpret_cast<Pack<DT, VEC>*>(static_cast<typename DT::Store*>(base) + at) = p;
 }
 
-// Sums of (a, b) over the row's threads: a warp (blockDim.y rows per block), or the block.
-__device__ __forceinline__ float2 row_sum(float a, float b, float2* s_red) {
+// A pack's values in fp32 and back: two 16-bit values per 32-bit word.
+template <class DT, int VEC>
+__device__ __forceinline__ void unpack(const Pack<DT, VEC>& p, float (&f)[VEC]) {
+  if constexpr (VEC == 8) {
+    const uint4 q = *reinterpret_cast<const uint4*>(&p);
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<DT, BF16>::value) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = load1(p.v[j], DT{});
+  }
+}
+template <class DT, int VEC>
+__device__ __forceinline__ Pack<DT, VEC> pack(const float (&f)[VEC]) {
+  Pack<DT, VEC> p;
+  if constexpr (VEC == 8) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<DT, BF16>::value) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      } else {
+        const __half2 v = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+    }
+    *reinterpret_cast<uint4*>(&p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) p.v[j] = store1(f[j], DT{});
+  }
+  return p;
+}
+
+template <int N>
+__device__ __forceinline__ void warp_sum(float (&v)[N]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    a += __shfl_xor_sync(0xffffffffu, a, o);
-    b += __shfl_xor_sync(0xffffffffu, b, o);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   }
+}
+
+// Sums of N values over the row's threads: a warp (blockDim.y rows per block), or the block.
+// The N values' chains of shuffles overlap: summing four rows at once costs little more than one.
+template <int N>
+__device__ __forceinline__ void row_sum(float (&v)[N], float* s_red) {
+  warp_sum(v);
   const int nw = blockDim.x >> 5;
-  if (nw == 1) return make_float2(a, b);
+  if (nw == 1) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();   // the previous sum has been read
-  if (lane == 0) s_red[warp] = make_float2(a, b);
-  __syncthreads();
-  float2 t = lane < nw ? s_red[lane] : make_float2(0.f, 0.f);
+  __syncthreads();   // the previous sums have been read
+  if (lane == 0) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    t.x += __shfl_xor_sync(0xffffffffu, t.x, o);
-    t.y += __shfl_xor_sync(0xffffffffu, t.y, o);
+    for (int i = 0; i < N; ++i) s_red[i * 32 + warp] = v[i];
   }
-  return t;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = lane < nw ? s_red[i * 32 + lane] : 0.f;
+  warp_sum(v);
+}
+
+// Asynchronous copies of a thread's own packs into its own slots of shared memory: rows come in
+// D - 1 steps ahead without holding registers, and no barrier is needed to read them.
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 struct NormParams {
@@ -88,143 +152,328 @@ struct NormParams {
   int32_t blocks;   // rows of `partial`
 };
 
-// NV packs per thread in registers; NV = 0: the row does not fit, and each pass reads it again.
-template <class DT, int VEC, int NV, bool LAYER>
-__global__ void __launch_bounds__(1024) norm_kernel(const NormParams p) {
-  __shared__ float2 s_red[32];
-  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
-  if (row >= p.T) return;   // (several rows per block only where a row is one warp: no block barrier)
-  const int n = p.d / VEC;
-  const int tid = threadIdx.x, step = blockDim.x;
-  constexpr int R = NV > 0 ? NV : 1;
-  Pack<DT, VEC> xv[R];
-  float s = 0.f;
-  if (NV > 0) {
+// VEC consecutive fp32 values (the packs of w, b and the column sums).
+template <int VEC>
+__device__ __forceinline__ void load_f32(const float* base, int at, float (&v)[VEC]) {
+  if (VEC == 1) {
+    v[0] = __ldg(base + at);
+  } else {
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int c = tid + k * step;
-      if (c < n) xv[k] = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)c * VEC);
+    for (int j = 0; j < VEC; j += 4) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(base + at + j));
+      v[j] = q.x;
+      v[j + 1 < VEC ? j + 1 : 0] = q.y;
+      v[j + 2 < VEC ? j + 2 : 0] = q.z;
+      v[j + 3 < VEC ? j + 3 : 0] = q.w;
     }
   }
-  auto each = [&](auto&& f) {   // f(k, pack index, pack)
-    if (NV > 0) {
+}
+
+// A warp per row, NV packs a lane: the row stays in registers and its sums need shuffles only.
+// The pass is bound by instructions before it is by HBM (16384 x 2880 in bf16: 63 us, at three
+// quarters of the issue slots, with a row on 12 warps, whose reductions each of them repeats).
+// w and b come from L1 as 16-byte loads.
+template <class DT, int VEC, int NV, bool LAYER>
+__global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
+  const int n = p.d / VEC, lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (row >= p.T) return;
+  Pack<DT, VEC> xv[NV];
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        const int c = tid + k * step;
-        if (c < n) f(c, xv[k]);
+  for (int k = 0; k < NV; ++k)
+    if (lane + 32 * k < n) xv[k] = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)(lane + 32 * k) * VEC);
+  float s[1] = {0.f}, q[1] = {0.f};
+  if (LAYER) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (lane + 32 * k < n) {
+        float f[VEC];
+        unpack<DT, VEC>(xv[k], f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s[0] += f[j];
       }
-    } else {
-      for (int c = tid; c < n; c += step) {
-        xv[0] = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)c * VEC);
-        f(c, xv[0]);
-      }
+    warp_sum(s);
+  }
+  const float m = s[0] * p.inv_d;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (lane + 32 * k < n) {
+      float f[VEC];
+      unpack<DT, VEC>(xv[k], f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) q[0] += (f[j] - m) * (f[j] - m);
     }
-  };
+  warp_sum(q);
+  const float r = 1.f / sqrtf(q[0] * p.inv_d + p.eps);
+  if (lane == 0) {
+    if (p.rstd) p.rstd[row] = r;
+    if (LAYER && p.mean) p.mean[row] = m;
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (lane + 32 * k < n) {
+      float f[VEC], w[VEC], b[VEC];
+      unpack<DT, VEC>(xv[k], f);
+      load_f32<VEC>(p.w, (lane + 32 * k) * VEC, w);
+      if (LAYER && p.b) load_f32<VEC>(p.b, (lane + 32 * k) * VEC, b);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        f[j] = (f[j] - m) * r * w[j];
+        if (LAYER && p.b) f[j] += b[j];
+      }
+      store_pack<DT, VEC>(p.y, row * p.ldy + (int64_t)(lane + 32 * k) * VEC, pack<DT, VEC>(f));
+    }
+}
+
+// A block per row (longer rows, and few rows: more loads in flight per row), NV packs a thread.
+template <class DT, int VEC, int NV, bool LAYER>
+__global__ void __launch_bounds__(512) norm_block_kernel(const NormParams p) {
+  __shared__ float s_red[32];
+  const int n = p.d / VEC, tid = threadIdx.x, step = blockDim.x;
+  const int64_t row = blockIdx.x;
+  Pack<DT, VEC> xv[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (tid + k * step < n) xv[k] = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)(tid + k * step) * VEC);
+  float s[1] = {0.f}, q[1] = {0.f};
+  if (LAYER) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (tid + k * step < n) {
+        float f[VEC];
+        unpack<DT, VEC>(xv[k], f);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s[0] += f[j];
+      }
+    row_sum<1>(s, s_red);
+  }
+  const float m = s[0] * p.inv_d;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (tid + k * step < n) {
+      float f[VEC];
+      unpack<DT, VEC>(xv[k], f);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) q[0] += (f[j] - m) * (f[j] - m);
+    }
+  row_sum<1>(q, s_red);
+  const float r = 1.f / sqrtf(q[0] * p.inv_d + p.eps);
+  if (tid == 0) {
+    if (p.rstd) p.rstd[row] = r;
+    if (LAYER && p.mean) p.mean[row] = m;
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (tid + k * step < n) {
+      float f[VEC], w[VEC], b[VEC];
+      unpack<DT, VEC>(xv[k], f);
+      load_f32<VEC>(p.w, (tid + k * step) * VEC, w);
+      if (LAYER && p.b) load_f32<VEC>(p.b, (tid + k * step) * VEC, b);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        f[j] = (f[j] - m) * r * w[j];
+        if (LAYER && p.b) f[j] += b[j];
+      }
+      store_pack<DT, VEC>(p.y, row * p.ldy + (int64_t)(tid + k * step) * VEC, pack<DT, VEC>(f));
+    }
+}
+
+// Rows too long for the registers of a block: each pass reads the row again (from L2).
+template <class DT, int VEC, bool LAYER>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
+  __shared__ float s_red[64];
+  const int64_t row = blockIdx.x;
+  const int n = p.d / VEC, tid = threadIdx.x, step = blockDim.x;
   float m = 0.f;
   if (LAYER) {
-    each([&](int, const Pack<DT, VEC>& v) {
+    float s = 0.f;
+    for (int c = tid; c < n; c += step) {
+      const Pack<DT, VEC> v = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)c * VEC);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) s += load1(v.v[j], DT{});
-    });
-    m = row_sum(s, 0.f, s_red).x * p.inv_d;
+    }
+    float v[1] = {s};
+    row_sum<1>(v, s_red);
+    m = v[0] * p.inv_d;
   }
   float q = 0.f;
-  each([&](int, const Pack<DT, VEC>& v) {
+  for (int c = tid; c < n; c += step) {
+    const Pack<DT, VEC> v = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)c * VEC);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       const float t = load1(v.v[j], DT{}) - m;
       q += t * t;
     }
-  });
-  const float r = 1.f / sqrtf(row_sum(q, 0.f, s_red).x * p.inv_d + p.eps);
+  }
+  float qs[1] = {q};
+  row_sum<1>(qs, s_red);
+  const float r = 1.f / sqrtf(qs[0] * p.inv_d + p.eps);
   if (tid == 0) {
     if (p.rstd) p.rstd[row] = r;
     if (LAYER && p.mean) p.mean[row] = m;
   }
-  each([&](int c, const Pack<DT, VEC>& v) {
+  for (int c = tid; c < n; c += step) {
+    const Pack<DT, VEC> v = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)c * VEC);
     Pack<DT, VEC> o;
+    float w[VEC], b[VEC];
+    load_f32<VEC>(p.w, c * VEC, w);
+    if (LAYER && p.b) load_f32<VEC>(p.b, c * VEC, b);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const int col = c * VEC + j;
-      float t = (load1(v.v[j], DT{}) - m) * r * __ldg(p.w + col);
-      if (LAYER && p.b) t += __ldg(p.b + col);
+      float t = (load1(v.v[j], DT{}) - m) * r * w[j];
+      if (LAYER && p.b) t += b[j];
       o.v[j] = store1(t, DT{});
     }
     store_pack<DT, VEC>(p.y, row * p.ldy + (int64_t)c * VEC, o);
-  });
+  }
 }
 
-// Rows blockIdx.x * blockDim.y + threadIdx.y, + gridDim.x * blockDim.y, ...; each thread keeps
-// the column sums of its own columns over its rows in registers, the block's rows meet in
-// shared memory, and each block writes one row of `partial`.
-template <class DT, int VEC, int NV, bool LAYER>
-__global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p) {
-  __shared__ float2 s_red[32];
+// The backward pass: a block takes R rows at a time (R groups of rows with short rows:
+// blockDim.y), and goes on to others; each thread keeps w and the column sums of its own columns
+// (NV packs) over all its rows in registers.  The block's row groups meet in shared memory, and
+// each block writes one row of `partial`.
+// D > 0: rows come through a D-deep ring of asynchronous copies into each thread's own slots, and
+// are read from there twice, which keeps the registers for the sums.  D = 0: loaded in place.
+template <class DT, int VEC, int NV, int R, int D, bool LAYER>
+__global__ void __launch_bounds__(576) norm_backward_kernel(const NormParams p) {
+  __shared__ float s_red[2 * R * 32];
+  extern __shared__ float4 s_dyn[];   // the ring, then the block's column sums (2 d floats)
+  const int threads = blockDim.x * blockDim.y, self = threadIdx.y * blockDim.x + threadIdx.x;
   const int n = p.d / VEC, tid = threadIdx.x, step = blockDim.x;
-  float aw[NV * VEC], ab[NV * VEC];
+  const int64_t stride = (int64_t)gridDim.x * blockDim.y * R;
+  using S = typename DT::Store;
+  float w[NV][VEC], aw[NV][VEC], ab[NV][VEC];
 #pragma unroll
-  for (int j = 0; j < NV * VEC; ++j) aw[j] = ab[j] = 0.f;
-  for (int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y; row < p.T; row += (int64_t)gridDim.x * blockDim.y) {
-    Pack<DT, VEC> xv[NV], dv[NV];
+  for (int k = 0; k < NV; ++k) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = tid + k * step;
-      if (c < n) {
-        xv[k] = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)c * VEC);
-        dv[k] = load_pack<DT, VEC>(p.dy, row * p.lddy + (int64_t)c * VEC);
+    for (int j = 0; j < VEC; ++j) aw[k][j] = ab[k][j] = 0.f;
+    if (tid + k * step < n) load_f32<VEC>(p.w, (tid + k * step) * VEC, w[k]);
+  }
+  const int64_t first = ((int64_t)blockIdx.x * blockDim.y + threadIdx.y) * R;
+  auto slot = [&](int stage, int i, int k, int t) {
+    return s_dyn + (((stage * R + i) * NV + k) * 3 + t) * threads + self;
+  };
+  auto bring = [&](int64_t row0, int stage) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t row = row0 + i;
+      if (row < p.T) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if (tid + k * step < n) {
+            const int64_t col = (int64_t)(tid + k * step) * VEC;
+            copy_async16(slot(stage, i, k, 0), static_cast<const S*>(p.x) + row * p.ldx + col);
+            copy_async16(slot(stage, i, k, 1), static_cast<const S*>(p.dy) + row * p.lddy + col);
+            if (p.dres) copy_async16(slot(stage, i, k, 2), static_cast<const S*>(p.dres) + row * p.lddres + col);
+          }
       }
     }
-    const float m = LAYER ? __ldg(p.mean + row) : 0.f, r = __ldg(p.rstd + row);
-    float c1 = 0.f, c2 = 0.f;
+    copy_commit();
+  };
+  int stage = 0;
+  if (D > 0) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = tid + k * step;
-      if (c < n) {
+    for (int s = 0; s < D - 1; ++s) bring(first + s * stride, s);
+  }
+  for (int64_t row0 = first; row0 < p.T; row0 += stride) {
+    Pack<DT, VEC> xv[R][NV] = {}, dv[R][NV] = {}, rv[R][NV] = {};   // (D = 0)
+    if (D > 0) {
+      bring(row0 + (D - 1) * stride, stage == 0 ? D - 1 : stage - 1);
+      copy_wait<(D > 0 ? D - 1 : 0)>();
+    }
+    auto get = [&](int i, int k, int t) {
+      if (D > 0) return *reinterpret_cast<const Pack<DT, VEC>*>(slot(stage, i, k, t));
+      return t == 0 ? xv[i][k] : t == 1 ? dv[i][k] : rv[i][k];
+    };
+    float mr[R], r[R], c[2 * R];   // xh = x r - m r
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (load1(xv[k].v[j], DT{}) - m) * r, dy = load1(dv[k].v[j], DT{});
-          const float g = dy * __ldg(p.w + c * VEC + j);
-          c1 += g * xh;
-          c2 += g;
-          aw[k * VEC + j] += dy * xh;
-          ab[k * VEC + j] += dy;
-        }
+    for (int i = 0; i < R; ++i) {
+      const int64_t row = min(row0 + i, (int64_t)p.T - 1);
+      r[i] = __ldg(p.rstd + row);
+      mr[i] = LAYER ? __ldg(p.mean + row) * r[i] : 0.f;
+      c[i] = c[R + i] = 0.f;
+      if (D == 0) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if (tid + k * step < n) {
+            const int64_t col = (int64_t)(tid + k * step) * VEC;
+            xv[i][k] = load_pack<DT, VEC>(p.x, row * p.ldx + col);
+            dv[i][k] = load_pack<DT, VEC>(p.dy, row * p.lddy + col);
+            if (p.dres) rv[i][k] = load_pack<DT, VEC>(p.dres, row * p.lddres + col);
+          }
       }
     }
-    const float2 t = row_sum(c1, c2, s_red);
-    c1 = t.x * p.inv_d;
-    c2 = LAYER ? t.y * p.inv_d : 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = tid + k * step;
-      if (c < n) {
-        Pack<DT, VEC> o, rv;
-        if (p.dres) rv = load_pack<DT, VEC>(p.dres, row * p.lddres + (int64_t)c * VEC);
+    for (int i = 0; i < R; ++i) {
+      if (row0 + i < p.T) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float xh = (load1(xv[k].v[j], DT{}) - m) * r;
-          const float g = load1(dv[k].v[j], DT{}) * __ldg(p.w + c * VEC + j);
-          float v = r * (g - xh * c1 - c2);
-          if (p.dres) v += load1(rv.v[j], DT{});
-          o.v[j] = store1(v, DT{});
-        }
-        store_pack<DT, VEC>(p.dx, row * p.lddx + (int64_t)c * VEC, o);
+        for (int k = 0; k < NV; ++k)
+          if (tid + k * step < n) {
+            float x[VEC], dy[VEC];
+            unpack<DT, VEC>(get(i, k, 0), x);
+            unpack<DT, VEC>(get(i, k, 1), dy);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {
+              const float xh = LAYER ? x[j] * r[i] - mr[i] : x[j] * r[i], g = dy[j] * w[k][j];
+              c[i] += g * xh;
+              aw[k][j] += dy[j] * xh;
+              if (LAYER) {
+                c[R + i] += g;
+                ab[k][j] += dy[j];
+              }
+            }
+          }
       }
     }
+    if (LAYER) {
+      row_sum<2 * R>(c, s_red);
+    } else {
+      float c1[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) c1[i] = c[i];
+      row_sum<R>(c1, s_red);
+#pragma unroll
+      for (int i = 0; i < R; ++i) c[i] = c1[i];
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t row = row0 + i;
+      if (row < p.T) {
+        const float c1 = -r[i] * c[i] * p.inv_d, c2 = LAYER ? -r[i] * c[R + i] * p.inv_d : 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if (tid + k * step < n) {
+            float x[VEC], dy[VEC];
+            unpack<DT, VEC>(get(i, k, 0), x);
+            unpack<DT, VEC>(get(i, k, 1), dy);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) {   // r (g - xh mean(g xh) - mean(g))
+              const float xh = LAYER ? x[j] * r[i] - mr[i] : x[j] * r[i];
+              dy[j] = fmaf(xh, c1, fmaf(dy[j] * w[k][j], r[i], c2));
+            }
+            if (p.dres) {
+              unpack<DT, VEC>(get(i, k, 2), x);
+#pragma unroll
+              for (int j = 0; j < VEC; ++j) dy[j] += x[j];
+            }
+            store_pack<DT, VEC>(p.dx, row * p.lddx + (int64_t)(tid + k * step) * VEC, pack<DT, VEC>(dy));
+          }
+      }
+    }
+    if (D > 0) stage = stage + 1 == D ? 0 : stage + 1;
   }
   if (!p.partial) return;
-  extern __shared__ float s_col[];   // [blockDim.y > 1 ? 2 * d : 0]
+  float* s_col = reinterpret_cast<float*>(s_dyn + D * R * NV * 3 * threads);   // [blockDim.y > 1 ? 2 * d : 0]
   float* out = p.partial + (int64_t)blockIdx.x * 2 * p.d;
   for (int g = 0; g < blockDim.y; ++g) {   // the block's row groups add up in order
     if (threadIdx.y == g) {
 #pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const int c = tid + k * step;
-        if (c < n) {
+      for (int k = 0; k < NV; ++k)
+        if (tid + k * step < n) {
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const int col = c * VEC + j;
-            float vw = aw[k * VEC + j], vb = ab[k * VEC + j];
+            const int col = (tid + k * step) * VEC + j;
+            float vw = aw[k][j], vb = ab[k][j];
             if (g > 0) {
               vw += s_col[col];
               vb += s_col[p.d + col];
@@ -238,7 +487,6 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p) 
             }
           }
         }
-      }
     }
     if (g + 1 < blockDim.y) __syncthreads();
   }
@@ -247,7 +495,7 @@ __global__ void __launch_bounds__(512) norm_backward_kernel(const NormParams p) 
 // Rows too long for registers: dx with the row read twice, and the column sums on their own.
 template <class DT, int VEC, bool LAYER>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormParams p) {
-  __shared__ float2 s_red[32];
+  __shared__ float s_red[64];
   const int64_t row = blockIdx.x;
   const int n = p.d / VEC, tid = threadIdx.x, step = blockDim.x;
   const float m = LAYER ? __ldg(p.mean + row) : 0.f, r = __ldg(p.rstd + row);
@@ -255,24 +503,29 @@ __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormPara
   for (int c = tid; c < n; c += step) {
     const Pack<DT, VEC> xv = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)c * VEC);
     const Pack<DT, VEC> dv = load_pack<DT, VEC>(p.dy, row * p.lddy + (int64_t)c * VEC);
+    float w[VEC];
+    load_f32<VEC>(p.w, c * VEC, w);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const float xh = (load1(xv.v[j], DT{}) - m) * r, g = load1(dv.v[j], DT{}) * __ldg(p.w + c * VEC + j);
+      const float xh = (load1(xv.v[j], DT{}) - m) * r, g = load1(dv.v[j], DT{}) * w[j];
       c1 += g * xh;
       c2 += g;
     }
   }
-  const float2 t = row_sum(c1, c2, s_red);
-  c1 = t.x * p.inv_d;
-  c2 = LAYER ? t.y * p.inv_d : 0.f;
+  float t[2] = {c1, c2};
+  row_sum<2>(t, s_red);
+  c1 = t[0] * p.inv_d;
+  c2 = LAYER ? t[1] * p.inv_d : 0.f;
   for (int c = tid; c < n; c += step) {
     const Pack<DT, VEC> xv = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)c * VEC);
     const Pack<DT, VEC> dv = load_pack<DT, VEC>(p.dy, row * p.lddy + (int64_t)c * VEC);
     Pack<DT, VEC> o, rv;
     if (p.dres) rv = load_pack<DT, VEC>(p.dres, row * p.lddres + (int64_t)c * VEC);
+    float w[VEC];
+    load_f32<VEC>(p.w, c * VEC, w);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      const float xh = (load1(xv.v[j], DT{}) - m) * r, g = load1(dv.v[j], DT{}) * __ldg(p.w + c * VEC + j);
+      const float xh = (load1(xv.v[j], DT{}) - m) * r, g = load1(dv.v[j], DT{}) * w[j];
       float v = r * (g - xh * c1 - c2);
       if (p.dres) v += load1(rv.v[j], DT{});
       o.v[j] = store1(v, DT{});
@@ -298,20 +551,22 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p) {
   p.partial[(int64_t)blockIdx.x * 2 * p.d + p.d + col] = ab;
 }
 
-// dw and db: the rows of `partial` added up; 8 warps take every eighth row, then meet in order.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const NormParams p) {
-  __shared__ float s_sum[8][32];
+// dw and db: the rows of `partial` added up; 16 warps take every sixteenth row, then meet in order.
+__global__ void __launch_bounds__(512) norm_reduce_kernel(const NormParams p) {
+  __shared__ float s_sum[16][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;   // of [dw | db]
   float v = 0.f;
-  if (c < 2 * (int64_t)p.d)
-    for (int b = warp; b < p.blocks; b += 8) v += p.partial[(int64_t)b * 2 * p.d + c];
+  if (c < 2 * (int64_t)p.d) {
+#pragma unroll 8
+    for (int b = warp; b < p.blocks; b += 16) v += p.partial[(int64_t)b * 2 * p.d + c];
+  }
   s_sum[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && c < 2 * (int64_t)p.d) {
     float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) t += s_sum[w][lane];
+    for (int w = 0; w < 16; ++w) t += s_sum[w][lane];
     if (c < p.d) {
       if (p.dw) p.dw[c] = t;
     } else if (p.db) {
@@ -350,35 +605,61 @@ bool vec_ok(const void* q, int64_t ld, int vec, int size) {
   return !q || ((reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % vec == 0 && vec * size == 16);
 }
 
-// A row's threads: whole warps, at most `nv` packs each; more than a block holds: 0.
+// A row's threads: whole warps, at most `nv` packs each; more than 512: 0 (the row is long).
 int row_threads(int packs, int nv) {
   const int t = ((packs + nv - 1) / nv + 31) / 32 * 32;
-  return t <= 1024 ? t : 0;
+  return t <= 512 ? t : 0;
+}
+
+template <class K>
+bool allow_smem(K kern, size_t bytes) {
+  return bytes <= 48 * 1024 ||
+         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
 }
 
 template <class DT, int VEC, bool LAYER>
 int forward_vec(const NormArgs& a) {
-  constexpr int NV = VEC == 1 ? 8 : 4;
   const NormParams p = params_of(a);
-  const int g = row_threads(a.d / VEC, NV);
-  const int rows = g == 32 ? 8 : 1;   // short rows: a warp each, eight to a block
-  const dim3 block(g ? g : 1024, rows), grid((unsigned)((a.T + rows - 1) / rows));
-  auto kern = g ? norm_kernel<DT, VEC, NV, LAYER> : norm_kernel<DT, VEC, 0, LAYER>;
+  const int packs = a.d / VEC;
+  void (*kern)(NormParams) = nullptr;
+  dim3 grid, block;
+  // A warp per row where the row fits a warp's registers (at most 12 packs a lane) and the rows
+  // are many; few rows are spread over blocks (16 x 2880: 2.2 us against 3 us).
+  if (a.T >= 2 * multiprocessors() && packs <= 32 * 12) {
+    kern = packs <= 64    ? norm_warp_kernel<DT, VEC, 2, LAYER>
+           : packs <= 128 ? norm_warp_kernel<DT, VEC, 4, LAYER>
+           : packs <= 256 ? norm_warp_kernel<DT, VEC, 8, LAYER>
+                          : norm_warp_kernel<DT, VEC, 12, LAYER>;
+    grid = dim3((unsigned)((a.T + 3) / 4));
+    block = dim3(128);
+  } else {
+    constexpr int NV = VEC == 1 ? 16 : 4;
+    const int g1 = row_threads(packs, 1), g = g1 ? g1 : row_threads(packs, NV);
+    kern = g1 ? norm_block_kernel<DT, VEC, 1, LAYER>
+           : g ? norm_block_kernel<DT, VEC, NV, LAYER> : norm_long_kernel<DT, VEC, LAYER>;
+    grid = dim3((unsigned)a.T);
+    block = dim3(g ? g : 1024);
+  }
   return launch_kernel(kern, grid, block, 0, a.stream, false, p) == cudaSuccess ? 1 : -1;
 }
 
 template <class DT, int VEC, bool LAYER>
 int backward_vec(const NormArgs& a) {
-  constexpr int NV = VEC == 8 ? 2 : VEC == 4 ? 4 : 8;
+  // Two packs a thread: half the warps of one pack, which each repeat a row's reductions.
+  constexpr int NV = VEC == 1 ? 8 : 2, R = VEC == 1 ? 1 : 2, D = VEC == 1 ? 0 : 2;
   NormParams p = params_of(a);
   const int g = row_threads(a.d / VEC, NV);
   int n = 1;
-  if (g && g <= 512) {
-    const int rows = g == 32 ? 8 : 1;
-    p.blocks = (int)std::min<int64_t>((a.T + rows - 1) / rows, norm_partial_rows(a.T, a.d));
-    if (launch_kernel(norm_backward_kernel<DT, VEC, NV, LAYER>, dim3((unsigned)p.blocks), dim3(g, rows),
-                      rows > 1 ? 8 * (size_t)a.d : 0, a.stream, false, p) != cudaSuccess)
-      return -1;
+  if (g) {
+    const int y = g == 32 ? 8 : 1;   // short rows: a warp each, eight groups to a block
+    // several rows at a time, and copies ahead, once every resident block has several to take
+    const bool many = a.T >= 8 * multiprocessors() * y;
+    const int64_t fit = (int64_t)multiprocessors() * std::max(1, 576 / (g * y)), rows = y * (many ? R : 1);
+    p.blocks = (int)std::min(std::min<int64_t>((a.T + rows - 1) / rows, fit), norm_partial_rows(a.T, a.d));
+    const size_t smem = (many ? (size_t)D * R * NV * 3 * 16 * g * y : 0) + (y > 1 ? 8 * (size_t)a.d : 0);
+    auto kern = many ? norm_backward_kernel<DT, VEC, NV, R, D, LAYER> : norm_backward_kernel<DT, VEC, NV, 1, 0, LAYER>;
+    if (!allow_smem(kern, smem)) return -1;
+    if (launch_kernel(kern, dim3((unsigned)p.blocks), dim3(g, y), smem, a.stream, false, p) != cudaSuccess) return -1;
   } else {
     p.blocks = (int)norm_partial_rows(a.T, a.d);
     // (the column sums first: dx may overwrite dy or x)
@@ -393,7 +674,7 @@ int backward_vec(const NormArgs& a) {
       return -1;
   }
   if (!p.partial) return n;
-  if (launch_kernel(norm_reduce_kernel, dim3((unsigned)((2 * (int64_t)a.d + 31) / 32)), dim3(256), 0, a.stream, false,
+  if (launch_kernel(norm_reduce_kernel, dim3((unsigned)((2 * (int64_t)a.d + 31) / 32)), dim3(512), 0, a.stream, false,
                     p) != cudaSuccess)
     return -1;
   return n + 1;
@@ -404,7 +685,7 @@ int dispatch_vec(const NormArgs& a, bool backward) {
   constexpr int size = sizeof(typename DT::Store), VEC = 16 / size;
   const bool v = a.d % VEC == 0 && vec_ok(a.x, a.ldx, VEC, size) && vec_ok(a.y, a.ldy, VEC, size) &&
                  vec_ok(a.dy, a.lddy, VEC, size) && vec_ok(a.dres, a.lddres, VEC, size) &&
-                 vec_ok(a.dx, a.lddx, VEC, size);
+                 vec_ok(a.dx, a.lddx, VEC, size) && vec_ok(a.w, VEC, VEC, size) && vec_ok(a.b, VEC, VEC, size);
   if (backward) return v ? backward_vec<DT, VEC, LAYER>(a) : backward_vec<DT, 1, LAYER>(a);
   return v ? forward_vec<DT, VEC, LAYER>(a) : forward_vec<DT, 1, LAYER>(a);
 }

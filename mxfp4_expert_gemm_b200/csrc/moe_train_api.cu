@@ -238,7 +238,7 @@ moe_status moe_norm_backward(int32_t kind, int32_t dtype, int32_t T, int32_t d, 
   moe::note_launches(0);
   moe_status st = check_norm(kind, dtype, T, d);
   if (st != MOE_OK) return st;
-  if (!aligned(dw, 4) || !aligned(db, 4)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(dw, 4) || !aligned(db, 4) || (db && kind == MOE_NORM_RMS)) return MOE_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (T > 0) {
     const uintptr_t size = dtype == MOE_DTYPE_F32 ? 4 : 2;

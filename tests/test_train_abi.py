@@ -92,7 +92,7 @@ def test_norm_refusals(L):
     assert _norm(L, T=0, x=None, y=None, w=None) == moe.MOE_OK
     for kw in (dict(dy=None), dict(x=None), dict(w=None), dict(rstd=None), dict(mean=None), dict(dx=None),
                dict(dy=257), dict(dres=256, lddres=60), dict(lddx=60), dict(ws=None), dict(ws=65544), dict(dw=2),
-               dict(dx=256, lddx=72), dict(dres=8192, lddres=72)):
+               dict(dx=256, lddx=72), dict(dres=8192, lddres=72), dict(kind=0)):
         assert _norm_backward(L, **kw) == BAD, kw
     need = moe.moe_norm_workspace_bytes(4, 64)
     assert need > 0 and _norm_backward(L, n=need - 1) == WS
