@@ -89,6 +89,68 @@ __device__ __forceinline__ Pack<DT, VEC> pack(const float (&f)[VEC]) {
   return p;
 }
 
+// Element-wise arithmetic of a pack's values, two per instruction (the packed fp32 operations of
+// sm_100): the backward pass is bound by issue slots before it is by HBM.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+template <int N>   // d = a * b + c
+__device__ __forceinline__ void vfma(float (&d)[N], const float (&a)[N], const float (&b)[N], const float (&c)[N]) {
+  if constexpr (N == 1) d[0] = fmaf(a[0], b[0], c[0]);
+  else
+#pragma unroll
+    for (int j = 0; j < N; j += 2) fma2(d[j], d[j + 1], a[j], a[j + 1], b[j], b[j + 1], c[j], c[j + 1]);
+}
+template <int N>   // d = a * b + c with scalars b and c
+__device__ __forceinline__ void vfma(float (&d)[N], const float (&a)[N], float b, float c) {
+  if constexpr (N == 1) d[0] = fmaf(a[0], b, c);
+  else
+#pragma unroll
+    for (int j = 0; j < N; j += 2) fma2(d[j], d[j + 1], a[j], a[j + 1], b, b, c, c);
+}
+template <int N>   // d = a * b + c with a scalar b
+__device__ __forceinline__ void vfma(float (&d)[N], const float (&a)[N], float b, const float (&c)[N]) {
+  if constexpr (N == 1) d[0] = fmaf(a[0], b, c[0]);
+  else
+#pragma unroll
+    for (int j = 0; j < N; j += 2) fma2(d[j], d[j + 1], a[j], a[j + 1], b, b, c[j], c[j + 1]);
+}
+template <int N>
+__device__ __forceinline__ void vmul(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+  if constexpr (N == 1) d[0] = a[0] * b[0];
+  else
+#pragma unroll
+    for (int j = 0; j < N; j += 2) mul2(d[j], d[j + 1], a[j], a[j + 1], b[j], b[j + 1]);
+}
+template <int N>
+__device__ __forceinline__ void vadd(float (&d)[N], const float (&a)[N], const float (&b)[N]) {
+  if constexpr (N == 1) d[0] = a[0] + b[0];
+  else
+#pragma unroll
+    for (int j = 0; j < N; j += 2) add2(d[j], d[j + 1], a[j], a[j + 1], b[j], b[j + 1]);
+}
+
 template <int N>
 __device__ __forceinline__ void warp_sum(float (&v)[N]) {
 #pragma unroll
@@ -112,6 +174,21 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* s_red) {
     for (int i = 0; i < N; ++i) s_red[i * 32 + warp] = v[i];
   }
   __syncthreads();
+  if (nw <= 8) {   // few warps: every thread adds their sums itself (broadcast reads, no shuffles)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4 a = *reinterpret_cast<const float4*>(s_red + i * 32), b = *reinterpret_cast<const float4*>(s_red + i * 32 + 4);
+      float t = a.x + a.y;
+      if (nw > 2) t += a.z;
+      if (nw > 3) t += a.w;
+      if (nw > 4) t += b.x;
+      if (nw > 5) t += b.y;
+      if (nw > 6) t += b.z;
+      if (nw > 7) t += b.w;
+      v[i] = t;
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = lane < nw ? s_red[i * 32 + lane] : 0.f;
   warp_sum(v);
@@ -174,7 +251,7 @@ __device__ __forceinline__ void load_f32(const float* base, int at, float (&v)[V
 // quarters of the issue slots, with a row on 12 warps, whose reductions each of them repeats).
 // w and b come from L1 as 16-byte loads.
 template <class DT, int VEC, int NV, bool LAYER>
-__global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
+__global__ void __launch_bounds__(128, 6) norm_warp_kernel(const NormParams p) {
   const int n = p.d / VEC, lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   if (row >= p.T) return;
@@ -201,7 +278,10 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
       float f[VEC];
       unpack<DT, VEC>(xv[k], f);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) q[0] += (f[j] - m) * (f[j] - m);
+      for (int j = 0; j < VEC; ++j) {
+        const float t = LAYER ? f[j] - m : f[j];
+        q[0] += t * t;
+      }
     }
   warp_sum(q);
   const float r = 1.f / sqrtf(q[0] * p.inv_d + p.eps);
@@ -218,7 +298,7 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
       if (LAYER && p.b) load_f32<VEC>(p.b, (lane + 32 * k) * VEC, b);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        f[j] = (f[j] - m) * r * w[j];
+        f[j] = (LAYER ? (f[j] - m) * r : f[j] * r) * w[j];
         if (LAYER && p.b) f[j] += b[j];
       }
       store_pack<DT, VEC>(p.y, row * p.ldy + (int64_t)(lane + 32 * k) * VEC, pack<DT, VEC>(f));
@@ -228,7 +308,7 @@ __global__ void __launch_bounds__(128) norm_warp_kernel(const NormParams p) {
 // A block per row (longer rows, and few rows: more loads in flight per row), NV packs a thread.
 template <class DT, int VEC, int NV, bool LAYER>
 __global__ void __launch_bounds__(512) norm_block_kernel(const NormParams p) {
-  __shared__ float s_red[32];
+  __shared__ __align__(16) float s_red[32];
   const int n = p.d / VEC, tid = threadIdx.x, step = blockDim.x;
   const int64_t row = blockIdx.x;
   Pack<DT, VEC> xv[NV];
@@ -254,7 +334,10 @@ __global__ void __launch_bounds__(512) norm_block_kernel(const NormParams p) {
       float f[VEC];
       unpack<DT, VEC>(xv[k], f);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) q[0] += (f[j] - m) * (f[j] - m);
+      for (int j = 0; j < VEC; ++j) {
+        const float t = LAYER ? f[j] - m : f[j];
+        q[0] += t * t;
+      }
     }
   row_sum<1>(q, s_red);
   const float r = 1.f / sqrtf(q[0] * p.inv_d + p.eps);
@@ -271,7 +354,7 @@ __global__ void __launch_bounds__(512) norm_block_kernel(const NormParams p) {
       if (LAYER && p.b) load_f32<VEC>(p.b, (tid + k * step) * VEC, b);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        f[j] = (f[j] - m) * r * w[j];
+        f[j] = (LAYER ? (f[j] - m) * r : f[j] * r) * w[j];
         if (LAYER && p.b) f[j] += b[j];
       }
       store_pack<DT, VEC>(p.y, row * p.ldy + (int64_t)(tid + k * step) * VEC, pack<DT, VEC>(f));
@@ -281,7 +364,7 @@ __global__ void __launch_bounds__(512) norm_block_kernel(const NormParams p) {
 // Rows too long for the registers of a block: each pass reads the row again (from L2).
 template <class DT, int VEC, bool LAYER>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
-  __shared__ float s_red[64];
+  __shared__ __align__(16) float s_red[64];
   const int64_t row = blockIdx.x;
   const int n = p.d / VEC, tid = threadIdx.x, step = blockDim.x;
   float m = 0.f;
@@ -336,7 +419,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
 // are read from there twice, which keeps the registers for the sums.  D = 0: loaded in place.
 template <class DT, int VEC, int NV, int R, int D, bool LAYER>
 __global__ void __launch_bounds__(576) norm_backward_kernel(const NormParams p) {
-  __shared__ float s_red[2 * R * 32];
+  __shared__ __align__(16) float s_red[2 * R * 32];
   extern __shared__ float4 s_dyn[];   // the ring, then the block's column sums (2 d floats)
   const int threads = blockDim.x * blockDim.y, self = threadIdx.y * blockDim.x + threadIdx.x;
   const int n = p.d / VEC, tid = threadIdx.x, step = blockDim.x;
@@ -375,6 +458,16 @@ __global__ void __launch_bounds__(576) norm_backward_kernel(const NormParams p) 
 #pragma unroll
     for (int s = 0; s < D - 1; ++s) bring(first + s * stride, s);
   }
+  float rn[R], mn[R];   // the next rows' statistics, loaded a step ahead
+  auto stats = [&](int64_t row0) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t row = min(row0 + i, (int64_t)p.T - 1);
+      rn[i] = __ldg(p.rstd + row);
+      mn[i] = LAYER ? __ldg(p.mean + row) : 0.f;
+    }
+  };
+  stats(first);
   for (int64_t row0 = first; row0 < p.T; row0 += stride) {
     Pack<DT, VEC> xv[R][NV] = {}, dv[R][NV] = {}, rv[R][NV] = {};   // (D = 0)
     if (D > 0) {
@@ -389,8 +482,8 @@ __global__ void __launch_bounds__(576) norm_backward_kernel(const NormParams p) 
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int64_t row = min(row0 + i, (int64_t)p.T - 1);
-      r[i] = __ldg(p.rstd + row);
-      mr[i] = LAYER ? __ldg(p.mean + row) * r[i] : 0.f;
+      r[i] = rn[i];
+      mr[i] = mn[i] * r[i];
       c[i] = c[R + i] = 0.f;
       if (D == 0) {
 #pragma unroll
@@ -406,25 +499,32 @@ __global__ void __launch_bounds__(576) norm_backward_kernel(const NormParams p) 
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       if (row0 + i < p.T) {
+        float s1[VEC], s2[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) s1[j] = s2[j] = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
           if (tid + k * step < n) {
-            float x[VEC], dy[VEC];
+            float x[VEC], dy[VEC], g[VEC];
             unpack<DT, VEC>(get(i, k, 0), x);
             unpack<DT, VEC>(get(i, k, 1), dy);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-              const float xh = LAYER ? x[j] * r[i] - mr[i] : x[j] * r[i], g = dy[j] * w[k][j];
-              c[i] += g * xh;
-              aw[k][j] += dy[j] * xh;
-              if (LAYER) {
-                c[R + i] += g;
-                ab[k][j] += dy[j];
-              }
+            vfma(x, x, r[i], -mr[i]);           // xh
+            vmul(g, dy, w[k]);
+            vfma(s1, g, x, s1);
+            vfma(aw[k], dy, x, aw[k]);
+            if (LAYER) {
+              vadd(s2, s2, g);
+              vadd(ab[k], ab[k], dy);
             }
           }
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          c[i] += s1[j];
+          c[R + i] += s2[j];
+        }
       }
     }
+    stats(row0 + stride);
     if (LAYER) {
       row_sum<2 * R>(c, s_red);
     } else {
@@ -446,15 +546,13 @@ __global__ void __launch_bounds__(576) norm_backward_kernel(const NormParams p) 
             float x[VEC], dy[VEC];
             unpack<DT, VEC>(get(i, k, 0), x);
             unpack<DT, VEC>(get(i, k, 1), dy);
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {   // r (g - xh mean(g xh) - mean(g))
-              const float xh = LAYER ? x[j] * r[i] - mr[i] : x[j] * r[i];
-              dy[j] = fmaf(xh, c1, fmaf(dy[j] * w[k][j], r[i], c2));
-            }
+            // r (g - xh mean(g xh) - mean(g)), xh = x r - m r
+            vmul(dy, dy, w[k]);
+            vfma(dy, dy, r[i], fmaf(-mr[i], c1, c2));
+            vfma(dy, x, c1 * r[i], dy);
             if (p.dres) {
               unpack<DT, VEC>(get(i, k, 2), x);
-#pragma unroll
-              for (int j = 0; j < VEC; ++j) dy[j] += x[j];
+              vadd(dy, dy, x);
             }
             store_pack<DT, VEC>(p.dx, row * p.lddx + (int64_t)(tid + k * step) * VEC, pack<DT, VEC>(dy));
           }
@@ -495,7 +593,7 @@ __global__ void __launch_bounds__(576) norm_backward_kernel(const NormParams p) 
 // Rows too long for registers: dx with the row read twice, and the column sums on their own.
 template <class DT, int VEC, bool LAYER>
 __global__ void __launch_bounds__(1024) norm_backward_long_kernel(const NormParams p) {
-  __shared__ float s_red[64];
+  __shared__ __align__(16) float s_red[64];
   const int64_t row = blockIdx.x;
   const int n = p.d / VEC, tid = threadIdx.x, step = blockDim.x;
   const float m = LAYER ? __ldg(p.mean + row) : 0.f, r = __ldg(p.rstd + row);
@@ -551,22 +649,22 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p) {
   p.partial[(int64_t)blockIdx.x * 2 * p.d + p.d + col] = ab;
 }
 
-// dw and db: the rows of `partial` added up; 16 warps take every sixteenth row, then meet in order.
-__global__ void __launch_bounds__(512) norm_reduce_kernel(const NormParams p) {
-  __shared__ float s_sum[16][32];
+// dw and db: the rows of `partial` added up; 32 warps take every 32nd row, then meet in order.
+__global__ void __launch_bounds__(1024) norm_reduce_kernel(const NormParams p) {
+  __shared__ float s_sum[32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;   // of [dw | db]
   float v = 0.f;
   if (c < 2 * (int64_t)p.d) {
-#pragma unroll 8
-    for (int b = warp; b < p.blocks; b += 16) v += p.partial[(int64_t)b * 2 * p.d + c];
+#pragma unroll 16
+    for (int b = warp; b < p.blocks; b += 32) v += p.partial[(int64_t)b * 2 * p.d + c];
   }
   s_sum[warp][lane] = v;
   __syncthreads();
   if (warp == 0 && c < 2 * (int64_t)p.d) {
     float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) t += s_sum[w][lane];
+    for (int w = 0; w < 32; ++w) t += s_sum[w][lane];
     if (c < p.d) {
       if (p.dw) p.dw[c] = t;
     } else if (p.db) {
@@ -674,7 +772,7 @@ int backward_vec(const NormArgs& a) {
       return -1;
   }
   if (!p.partial) return n;
-  if (launch_kernel(norm_reduce_kernel, dim3((unsigned)((2 * (int64_t)a.d + 31) / 32)), dim3(512), 0, a.stream, false,
+  if (launch_kernel(norm_reduce_kernel, dim3((unsigned)(((a.layer ? 2 : 1) * (int64_t)a.d + 31) / 32)), dim3(1024), 0, a.stream, false,
                     p) != cudaSuccess)
     return -1;
   return n + 1;
