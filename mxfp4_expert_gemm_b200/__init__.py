@@ -482,92 +482,106 @@ def moe_debug_inject_timeout(enable: bool = True) -> None:
 
 
 # ----------------------------------------------------------- norms and 16-bit products, with gradients
-def _rows(t: torch.Tensor, dtype, name, device, shape=None) -> int:
-    """Row stride of a [rows, columns] tensor whose columns are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+# These calls are short enough on the GPU (2-10 us) for the host's part to show, so their checks
+# read a tensor's properties once and the stream as a plain handle.
+try:
+    from torch._C import _cuda_getCurrentRawStream as _current_raw_stream
+except ImportError:
+    def _current_raw_stream(device: int) -> int:
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _here(t, name) -> int:
+    """The device index of a call's first tensor, which has to be the current one."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
         raise TypeError(f"{name}: a CUDA tensor is required")
-    if t.dtype != dtype:
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _rows(t, dtype, name, dev, rows, cols) -> int:
+    """Row stride of a [rows, cols] tensor whose columns are contiguous."""
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        raise TypeError(f"{name}: a CUDA tensor is required")
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.dim() != 2 or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape) if shape else '[rows, columns]'}")
-    rows, cols = t.shape
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
     ld, one = t.stride()
     if one != 1 and cols != 1:
         raise ValueError(f"{name}: the columns of a row must be contiguous")
-    if rows <= 1 and ld < cols:
-        return cols
-    return ld
+    return cols if rows <= 1 and ld < cols else ld
 
 
-def _flat(t, dtype, name, device, shape):
-    """A contiguous tensor of the given shape, or None."""
+def _flat(t, dtype, name, dev, shape):
+    """The address of a contiguous tensor of the given shape (None for None)."""
     if t is None:
         return None
-    _need(t, dtype, name, shape)
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
+        raise TypeError(f"{name}: a CUDA tensor is required")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
     return t.data_ptr()
 
 
-def _here(t, name) -> torch.device:
-    """The device of a call's first tensor, which has to be the current one."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name}: a CUDA tensor is required")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+def _raw_stream(stream, dev) -> int:
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _raw_stream(stream) -> int:
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _status(status_word, dev):
+    return None if status_word is None else _flat(status_word, torch.int32, "status_word", dev, status_word.shape)
 
 
-def _status(status_word, device):
-    if status_word is None:
-        return None
-    _need(status_word, torch.int32, "status_word")
-    if status_word.device != device:
-        raise ValueError(f"status_word: on {status_word.device}, expected {device}")
-    return status_word.data_ptr()
-
-
-def _workspace(ws, nbytes, device):
-    """(pointer, bytes) of a caller's workspace, or of one taken from torch's allocator."""
+def _workspace(ws, nbytes, like, dev):
+    """(tensor, address, bytes) of a caller's workspace, or of one taken from torch's allocator."""
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    elif ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws: a contiguous tensor on {device} is required")
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous tensor on cuda:{dev} is required")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _norm_kind(kind) -> int:
-    if kind not in NORM_KINDS:
+def _norm_args(x, kind):
+    dev = _here(x, "x")
+    dt = DTYPES.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x: dtype {x.dtype}")
+    k = NORM_KINDS.get(kind)
+    if k is None:
         raise ValueError(f"kind: {kind!r}, expected one of {sorted(NORM_KINDS)}")
-    return NORM_KINDS[kind]
+    if x.dim() != 2:
+        raise ValueError(f"x: shape {tuple(x.shape)}, expected [rows, columns]")
+    T, d = x.shape
+    return dev, dt, k, T, d, _rows(x, x.dtype, "x", dev, T, d)
 
 
 def moe_norm(x, w, b=None, kind="rms", eps=1e-5, y=None, want_stats=False, stream=None):
     """y [T, d] = RMSNorm(x) * w (kind "rms") or LayerNorm(x) * w + b (kind "layer"); bf16, fp16
     or fp32 rows, fp32 w and b.  With want_stats: (y, mean, rstd) for moe_norm_backward (mean is
     None for "rms")."""
-    dev = _here(x, "x")
-    if x.dtype not in DTYPES:
-        raise TypeError(f"x: dtype {x.dtype}")
-    k = _norm_kind(kind)
-    ldx = _rows(x, x.dtype, "x", dev)
-    T, d = x.shape
+    dev, dt, k, T, d, ldx = _norm_args(x, kind)
     if y is None:
-        y = torch.empty((T, d), dtype=x.dtype, device=dev)
+        y, ldy = x.new_empty((T, d)), d
+    else:
+        ldy = _rows(y, x.dtype, "y", dev, T, d)
     mean = rstd = None
     if want_stats:
-        stats = torch.empty((2, T), dtype=torch.float32, device=dev)
-        rstd, mean = stats[0], stats[1] if k == 1 else None
-    _check(lib().moe_norm(k, DTYPES[x.dtype], T, d, x.data_ptr(), ldx, _flat(w, torch.float32, "w", dev, (d,)),
-                          _flat(b, torch.float32, "b", dev, (d,)), eps, y.data_ptr(),
-                          _rows(y, x.dtype, "y", dev, x.shape), None if mean is None else mean.data_ptr(),
-                          None if rstd is None else rstd.data_ptr(), _raw_stream(stream)), "moe_norm")
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        mean = torch.empty_like(rstd) if k == 1 else None
+    _check((_lib or lib()).moe_norm(k, dt, T, d, x.data_ptr(), ldx, _flat(w, torch.float32, "w", dev, (d,)),
+                                    _flat(b, torch.float32, "b", dev, (d,)), eps, y.data_ptr(), ldy,
+                                    None if mean is None else mean.data_ptr(),
+                                    None if rstd is None else rstd.data_ptr(), _raw_stream(stream, dev)), "moe_norm")
     return (y, mean, rstd) if want_stats else y
 
 
@@ -578,32 +592,28 @@ def moe_norm_workspace_bytes(T: int, d: int) -> int:
 def moe_norm_backward(dy, x, w, mean, rstd, kind="rms", dres=None, dx=None, need_dw=True, need_db=None, ws=None,
                       stream=None):
     """(dx, dw, db) of moe_norm, with dres (a gradient of dx's shape) added to dx in the same pass.
-    dw and db are fp32 [d]; db defaults to kind == "layer" and is None when not asked for."""
-    dev = _here(x, "x")
-    if x.dtype not in DTYPES:
-        raise TypeError(f"x: dtype {x.dtype}")
-    k = _norm_kind(kind)
-    ldx = _rows(x, x.dtype, "x", dev)
-    T, d = x.shape
+    dw and db are fp32 [d]; db ("layer" only) defaults to kind == "layer" and is None when not
+    asked for."""
+    dev, dt, k, T, d, ldx = _norm_args(x, kind)
     if need_db is None:
         need_db = k == 1
-    lddy = _rows(dy, x.dtype, "dy", dev, x.shape)
-    lddres = 0 if dres is None else _rows(dres, x.dtype, "dres", dev, x.shape)
+    lddy = _rows(dy, x.dtype, "dy", dev, T, d)
+    lddres = 0 if dres is None else _rows(dres, x.dtype, "dres", dev, T, d)
     if dx is None:
-        dx = torch.empty((T, d), dtype=x.dtype, device=dev)
-    dw = torch.empty(d, dtype=torch.float32, device=dev) if need_dw else None
-    db = torch.empty(d, dtype=torch.float32, device=dev) if need_db else None
+        dx, lddx = x.new_empty((T, d)), d
+    else:
+        lddx = _rows(dx, x.dtype, "dx", dev, T, d)
+    dw = torch.empty(d, dtype=torch.float32, device=x.device) if need_dw else None
+    db = torch.empty(d, dtype=torch.float32, device=x.device) if need_db else None
     ws_ptr, ws_bytes = None, 0
     if need_dw or need_db:
-        ws, ws_ptr, ws_bytes = _workspace(ws, moe_norm_workspace_bytes(T, d), dev)
-    _check(lib().moe_norm_backward(k, DTYPES[x.dtype], T, d, dy.data_ptr(), lddy, x.data_ptr(), ldx,
-                                   _flat(w, torch.float32, "w", dev, (d,)),
-                                   _flat(mean, torch.float32, "mean", dev, (T,)),
-                                   _flat(rstd, torch.float32, "rstd", dev, (T,)),
-                                   None if dres is None else dres.data_ptr(), lddres, dx.data_ptr(),
-                                   _rows(dx, x.dtype, "dx", dev, x.shape), None if dw is None else dw.data_ptr(),
-                                   None if db is None else db.data_ptr(), ws_ptr, ws_bytes, _raw_stream(stream)),
-           "moe_norm_backward")
+        ws, ws_ptr, ws_bytes = _workspace(ws, moe_norm_workspace_bytes(T, d), x, dev)
+    _check((_lib or lib()).moe_norm_backward(
+        k, dt, T, d, dy.data_ptr(), lddy, x.data_ptr(), ldx, _flat(w, torch.float32, "w", dev, (d,)),
+        _flat(mean, torch.float32, "mean", dev, (T,)), _flat(rstd, torch.float32, "rstd", dev, (T,)),
+        None if dres is None else dres.data_ptr(), lddres, dx.data_ptr(), lddx,
+        None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), ws_ptr, ws_bytes,
+        _raw_stream(stream, dev)), "moe_norm_backward")
     return dx, dw, db
 
 
@@ -622,38 +632,41 @@ def moe_linear_workspace_bytes(dims: moe_linear_dims, rows: int) -> int:
 
 
 def _product_dims(x, w, grouped, fn, limit):
-    """(device, row stride of x, dims) of a product's x [rows, K] and w [N, K] ([E, N, K])."""
+    """(device, rows, row stride of x, dims) of a product's x [rows, K] and w [N, K] ([E, N, K])."""
     dev = _here(x, "x")
-    ldx = _rows(x, x.dtype, "x", dev)
-    want = 3 if grouped else 2
-    if not isinstance(w, torch.Tensor) or w.dim() != want or w.shape[-1] != x.shape[1]:
-        raise ValueError(f"w: a tensor {'[E, N, K]' if grouped else '[N, K]'} with K = {x.shape[1]} is required")
+    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != (3 if grouped else 2) or w.shape[-1] != x.shape[1]:
+        raise ValueError(f"x [rows, K] and w {'[E, N, K]' if grouped else '[N, K]'} are required")
+    rows, K = x.shape
+    ldx = _rows(x, x.dtype, "x", dev, rows, K)
     _flat(w, x.dtype, "w", dev, w.shape)
-    return dev, ldx, make_linear_dims(x.shape[1], w.shape[-2], w.shape[0] if grouped else 1, x.dtype, fn, limit)
+    return dev, rows, ldx, make_linear_dims(K, w.shape[-2], w.shape[0] if grouped else 1, x.dtype, fn, limit)
 
 
 def _forward_product(what, x, w, offsets, bias, fn, limit, residual, y, z, want_z, status_word, stream):
     grouped = offsets is not None
-    dev, ldx, dims = _product_dims(x, w, grouped, fn, limit)
-    rows, N = x.shape[0], dims.N
+    dev, rows, ldx, dims = _product_dims(x, w, grouped, fn, limit)
+    N = dims.N
     No = N // 2 if fn == "swiglu" else N
     if y is None:
-        y = torch.empty((rows, No), dtype=x.dtype, device=dev)
+        y, ldy = x.new_empty((rows, No)), No
+    else:
+        ldy = _rows(y, x.dtype, "y", dev, rows, No)
     if want_z and z is None:
-        z = torch.empty((rows, N), dtype=x.dtype, device=dev)
-    ldy = _rows(y, x.dtype, "y", dev, (rows, No))
+        z = x.new_empty((rows, N))
     zp = _flat(z, x.dtype, "z", dev, (rows, N))
     bp = _flat(bias, torch.float32, "bias", dev, (dims.E, N) if grouped else (N,))
     sp = _status(status_word, dev)
+    L = _lib or lib()
     if grouped:
         op = _flat(offsets, torch.int32, "offsets", dev, (dims.E + 1,))
-        st = lib().moe_grouped_linear(ctypes.byref(dims), rows, x.data_ptr(), ldx, w.data_ptr(), op, bp, y.data_ptr(),
-                                      ldy, zp, sp, _raw_stream(stream))
+        st = L.moe_grouped_linear(ctypes.byref(dims), rows, x.data_ptr(), ldx, w.data_ptr(), op, bp, y.data_ptr(), ldy,
+                                  zp, sp, _raw_stream(stream, dev))
     else:
-        ldr = 0 if residual is None else _rows(residual, x.dtype, "residual", dev, (rows, No))
-        st = lib().moe_linear(ctypes.byref(dims), rows, x.data_ptr(), ldx, w.data_ptr(), bp,
-                              None if residual is None else residual.data_ptr(), ldr, y.data_ptr(), ldy, zp, sp,
-                              _raw_stream(stream))
+        rp, ldr = None, 0
+        if residual is not None:
+            rp, ldr = residual.data_ptr(), _rows(residual, x.dtype, "residual", dev, rows, No)
+        st = L.moe_linear(ctypes.byref(dims), rows, x.data_ptr(), ldx, w.data_ptr(), bp, rp, ldr, y.data_ptr(), ldy, zp,
+                          sp, _raw_stream(stream, dev))
     _check(st, what)
     return (y, z) if want_z else y
 
@@ -661,34 +674,40 @@ def _forward_product(what, x, w, offsets, bias, fn, limit, residual, y, z, want_
 def _backward_product(what, dy, x, w, offsets, z, fn, limit, dx, dw, need_dx, need_dw, need_db, ws, status_word,
                       stream):
     grouped = offsets is not None
-    dev, ldx, dims = _product_dims(x, w, grouped, fn, limit)
-    rows, K, N = x.shape[0], dims.K, dims.N
-    lddy = _rows(dy, x.dtype, "dy", dev, (rows, N // 2 if fn == "swiglu" else N))
+    dev, rows, ldx, dims = _product_dims(x, w, grouped, fn, limit)
+    K, N = dims.K, dims.N
+    lddy = _rows(dy, x.dtype, "dy", dev, rows, N // 2 if fn == "swiglu" else N)
     if fn != "none" and z is None:
         raise ValueError(f"z: the forward pass's pre-activation is required with fn={fn!r}")
     zp = _flat(z, x.dtype, "z", dev, (rows, N)) if fn != "none" else None
-    need_dx, need_dw = need_dx or dx is not None, need_dw or dw is not None
-    if need_dx and dx is None:
-        dx = torch.empty((rows, K), dtype=x.dtype, device=dev)
-    if need_dw and dw is None:
-        dw = torch.empty(w.shape, dtype=x.dtype, device=dev)
-    lddx = _rows(dx, x.dtype, "dx", dev, (rows, K)) if need_dx else 0
-    dwp = _flat(dw, x.dtype, "dw", dev, w.shape) if need_dw else None
-    db = torch.empty(w.shape[:-1], dtype=torch.float32, device=dev) if need_db else None
+    dxp, lddx, dwp, db, dbp = None, 0, None, None, None
+    if dx is not None:
+        dxp, lddx = dx.data_ptr(), _rows(dx, x.dtype, "dx", dev, rows, K)
+    elif need_dx:
+        dx, lddx = x.new_empty((rows, K)), K
+        dxp = dx.data_ptr()
+    if dw is not None:
+        dwp = _flat(dw, x.dtype, "dw", dev, w.shape)
+    elif need_dw:
+        dw = torch.empty_like(w)
+        dwp = dw.data_ptr()
+    if need_db:
+        db = torch.empty(w.shape[:-1], dtype=torch.float32, device=x.device)
+        dbp = db.data_ptr()
     ws_ptr, ws_bytes = None, 0
     if fn != "none" or need_db:
-        ws, ws_ptr, ws_bytes = _workspace(ws, moe_linear_workspace_bytes(dims, rows), dev)
-    common = (zp, dx.data_ptr() if need_dx else None, lddx, dwp, db.data_ptr() if need_db else None, ws_ptr, ws_bytes,
-              _status(status_word, dev), _raw_stream(stream))
+        ws, ws_ptr, ws_bytes = _workspace(ws, moe_linear_workspace_bytes(dims, rows), x, dev)
+    common = (zp, dxp, lddx, dwp, dbp, ws_ptr, ws_bytes, _status(status_word, dev), _raw_stream(stream, dev))
+    L = _lib or lib()
     if grouped:
         op = _flat(offsets, torch.int32, "offsets", dev, (dims.E + 1,))
-        st = lib().moe_grouped_linear_backward(ctypes.byref(dims), rows, dy.data_ptr(), lddy, x.data_ptr(), ldx,
-                                               w.data_ptr(), op, *common)
+        st = L.moe_grouped_linear_backward(ctypes.byref(dims), rows, dy.data_ptr(), lddy, x.data_ptr(), ldx,
+                                           w.data_ptr(), op, *common)
     else:
-        st = lib().moe_linear_backward(ctypes.byref(dims), rows, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(),
-                                       *common)
+        st = L.moe_linear_backward(ctypes.byref(dims), rows, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(),
+                                   *common)
     _check(st, what)
-    return dx if need_dx else None, dw if need_dw else None, db
+    return dx, dw, db
 
 
 def moe_linear(x, w, bias=None, fn="none", limit=7.0, residual=None, y=None, z=None, want_z=False, status_word=None,

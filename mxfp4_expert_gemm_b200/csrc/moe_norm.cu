@@ -260,15 +260,19 @@ __global__ void __launch_bounds__(128, 6) norm_warp_kernel(const NormParams p) {
   for (int k = 0; k < NV; ++k)
     if (lane + 32 * k < n) xv[k] = load_pack<DT, VEC>(p.x, row * p.ldx + (int64_t)(lane + 32 * k) * VEC);
   float s[1] = {0.f}, q[1] = {0.f};
+  float acc[VEC], qcc[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) acc[j] = qcc[j] = 0.f;
   if (LAYER) {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
       if (lane + 32 * k < n) {
         float f[VEC];
         unpack<DT, VEC>(xv[k], f);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) s[0] += f[j];
+        vadd(acc, acc, f);
       }
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s[0] += acc[j];
     warp_sum(s);
   }
   const float m = s[0] * p.inv_d;
@@ -277,12 +281,11 @@ __global__ void __launch_bounds__(128, 6) norm_warp_kernel(const NormParams p) {
     if (lane + 32 * k < n) {
       float f[VEC];
       unpack<DT, VEC>(xv[k], f);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const float t = LAYER ? f[j] - m : f[j];
-        q[0] += t * t;
-      }
+      if (LAYER) vfma(f, f, 1.f, -m);
+      vfma(qcc, f, f, qcc);
     }
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) q[0] += qcc[j];
   warp_sum(q);
   const float r = 1.f / sqrtf(q[0] * p.inv_d + p.eps);
   if (lane == 0) {
@@ -295,11 +298,13 @@ __global__ void __launch_bounds__(128, 6) norm_warp_kernel(const NormParams p) {
       float f[VEC], w[VEC], b[VEC];
       unpack<DT, VEC>(xv[k], f);
       load_f32<VEC>(p.w, (lane + 32 * k) * VEC, w);
-      if (LAYER && p.b) load_f32<VEC>(p.b, (lane + 32 * k) * VEC, b);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        f[j] = (LAYER ? (f[j] - m) * r : f[j] * r) * w[j];
-        if (LAYER && p.b) f[j] += b[j];
+      if (LAYER) vfma(f, f, 1.f, -m);
+      vfma(f, f, r, 0.f);
+      if (LAYER && p.b) {
+        load_f32<VEC>(p.b, (lane + 32 * k) * VEC, b);
+        vfma(f, f, w, b);
+      } else {
+        vmul(f, f, w);
       }
       store_pack<DT, VEC>(p.y, row * p.ldy + (int64_t)(lane + 32 * k) * VEC, pack<DT, VEC>(f));
     }
