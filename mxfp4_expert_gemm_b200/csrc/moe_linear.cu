@@ -506,6 +506,7 @@ struct SplitCfg {
   static constexpr int SMEM = S * STAGE + BAR_BYTES + 1024 /* align slack */;
   static constexpr int THREADS = 32 * 6;                // producer, MMA, four epilogue warps
   static_assert(EPI_OFF + kEpiBytes <= S * STAGE, "the partial tile and the epilogue's buffer fit the stages");
+  static_assert(!SPLIT || EPI_OFF + 32 * 512 <= S * STAGE, "a sum's reads past its share stay in the stages");
   static_assert((SMEM + 1024) * CPS <= 228 * 1024, "shared memory of the co-resident CTAs");
   static_assert((NB == 32 || NB == 64 || NB == 128) && (!B_MN || NB % 64 == 0), "tile width");
 };
@@ -703,14 +704,21 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
         part.nj = c1;
         const float* red = dst + row;
         for (int c0 = rank * per; c0 < c1; c0 += 32) {
+          // One rank's 32 columns at a time, in straight-line code: a loop over the ranks inside
+          // each column ran cold instructions column by column, 17 us for 32 of them.  Columns past
+          // the share read what lies there and are not stored.
+          float sum[32];
           uint32_t v[32];
 #pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            float sum = 0.f;
-            if (c0 + c < c1)
-              for (int r = 0; r < S; ++r) sum += red[(r * per + c0 + c - rank * per) * 128];
-            v[c] = __float_as_uint(sum);
+          for (int c = 0; c < 32; ++c) sum[c] = 0.f;
+#pragma unroll 1
+          for (int r = 0; r < S; ++r) {
+            const float* q = red + (r * per + c0 - rank * per) * 128;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) sum[c] += q[c * 128];
           }
+#pragma unroll
+          for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(sum[c]);
           finish<MODE, SW, BF>(p, part, v, bias, c0, row, smem + C::EPI_OFF, 2);
         }
       } else {
@@ -1070,11 +1078,13 @@ int launch_split_of(const LinArgs& a) {
   p.nw_max = NB;
   p.n_jt = (a.N + NB - 1) / NB;
   const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, NB)) * p.n_it;
-  // Fewer tiles than the GPU holds CTAs: a cluster shares each tile's contraction, every CTA
-  // keeping at least two 64-wide blocks of it.
+  // Fewer tiles than SMs: a cluster of up to four CTAs shares each tile's contraction (1 x 2880 x
+  // 2880: 15.0 / 11.2 / 9.0 / 9.6 us with 1 / 2 / 4 / 6), each keeping at least five 64-wide blocks
+  // of it (192-wide contractions: 5 us alone, 7 us shared), while the CTAs stay within 1.25 per
+  // SM (128 x 2880 x 2880, 46 tiles: 12.7 us with 3, 19.4 us with 6: the clusters then queue).
   const int64_t blocks = MODE == kWeightGrad ? (a.rows / (a.offsets ? a.E : 1) + kBK - 1) / kBK : (p.C + kBK - 1) / kBK;
-  int64_t s = std::min<int64_t>((int64_t)multiprocessors() * C::CPS / tiles, blocks / 2);
-  p.splits = C::SPLIT ? (int)std::max<int64_t>(1, std::min<int64_t>(s, 8)) : 1;
+  const int64_t s = std::min<int64_t>(5 * (int64_t)multiprocessors() / (4 * tiles), blocks / 5);
+  p.splits = C::SPLIT ? (int)std::max<int64_t>(1, std::min<int64_t>(s, 4)) : 1;
   auto kern = lin_split_kernel<MODE, SW, NB, BF>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, C::SMEM, done)) return -1;
@@ -1190,14 +1200,13 @@ int launch_linear(const LinArgs& a) {
 
 // ------------------------------------------------------------------------------ activation gradient
 // dz = dy f'(z) and the column sums db of dz, in one pass over dy and z.  A block takes a chunk
-// of kChunk rows of one expert and 256 columns, 8 per lane; its 8 warps take rows in turn and
+// of kChunk rows of one expert and 256 columns of dy, 8 per lane; its 8 warps take rows in turn and
 // add their column sums in a fixed order into one row of `partial`, which sum_chunks_kernel
 // adds up per expert.  The sums take dz before its rounding to 16 bits.
 namespace {
 constexpr int kChunk = 64;
 
 __device__ __forceinline__ float from16r(uint16_t v, bool bf) { return bf ? from16<true>(v) : from16<false>(v); }
-__device__ __forceinline__ uint16_t to16r(float v, bool bf) { return bf ? to16<true>(v) : to16<false>(v); }
 
 struct ActGradParams {
   int32_t rows, N, No, E, bf16, fn, chunks;
@@ -1219,8 +1228,16 @@ __device__ __forceinline__ float act_grad(float z, float dy) {
     const float s = __fdividef(1.f, 1.f + __expf(-z));
     return dy * s * (1.f + z * (1.f - s));
   }
-  if (FN == MOE_FN_GELU)
-    return dy * (0.5f * erfcf(-0.70710678f * z) + z * __expf(-0.5f * z * z) * 0.39894228f);
+  if (FN == MOE_FN_GELU) {
+    // erfc(x) = t (a1 + t (a2 + ...)) exp(-x^2), t = 1 / (1 + 0.3275911 x) for x >= 0 to 1.5e-7
+    // (Abramowitz and Stegun 7.1.26), shares its exponential with the density: 0.75e-7 of dy,
+    // against 2^-12 of dz's own rounding (4099 x 4096: 47 us with erfcf).
+    const float x = fabsf(z) * 0.70710678f, e = __expf(-0.5f * z * z);
+    const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+    const float q = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f),
+                             0.254829592f) * e * 0.5f;   // erfc(|z| / sqrt 2) / 2
+    return dy * (fmaf(z * e, 0.39894228f, z < 0.f ? q : 1.f - q));
+  }
   if (FN == MOE_FN_GELU_TANH) {   // s = (1 + tanh v) / 2, (1 - tanh^2 v) / 2 = 2 s (1 - s)
     const float s = __fdividef(1.f, 1.f + __expf(-2.f * gelu_arg(z)));
     return dy * (s + 2.f * z * s * (1.f - s) * 0.79788456f * (1.f + 0.134145f * z * z));
@@ -1245,9 +1262,42 @@ __device__ __forceinline__ bool find_chunk(const ActGradParams& p, int q, int& e
   return t.ok != 0;
 }
 
+// Eight values of dz from those of dy and z (SwiGLU: d_g and d_u from g and u).
+template <int FN>
+__device__ __forceinline__ void act_grad8(const ActGradParams& p, const float (&z)[8], const float (&u)[8],
+                                          const float (&dy)[8], float (&o)[8], float (&ou)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (FN == MOE_FN_SWIGLU) {
+      const float g = clamp_hi(z[k], p.limit), uc = clamp_both(u[k], p.limit);
+      const float s = __fdividef(1.f, 1.f + __expf(-g)), gs = g * s;
+      o[k] = z[k] > p.limit ? 0.f : dy[k] * uc * (s + gs * (1.f - s));
+      ou[k] = fabsf(u[k]) <= p.limit ? dy[k] * gs : 0.f;
+    } else {
+      o[k] = act_grad<FN>(z[k], dy[k]);
+    }
+  }
+}
+
+__device__ __forceinline__ void widen(const uint4& q, bool bf, float (&f)[8]) {
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(&q);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = from16r(h[k], bf);
+}
+__device__ __forceinline__ uint4 narrow(const float (&f)[8], bool bf) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    w[k] = bf ? to16x2<true>(f[2 * k], f[2 * k + 1]) : to16x2<false>(f[2 * k], f[2 * k + 1]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Threads: 32 lanes of 8 columns of dy (SwiGLU: the gate and the up column both), 8 warps of rows;
+// two rows of a warp are loaded together.
 template <int FN>
 __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
-  __shared__ int s_t[4];
+  constexpr int H = FN == MOE_FN_SWIGLU ? 2 : 1;
+  __shared__ int s_t[3];
   __shared__ float s_sum[8][256];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
@@ -1261,63 +1311,59 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
   }
   __syncthreads();
   if (!s_t[0]) return;
-  const int r0 = s_t[1], n = s_t[2];
+  const int r0 = s_t[1], r1 = r0 + s_t[2];
   const bool bf = p.bf16 != 0;
-  const int col = blockIdx.y * 256 + 8 * lane;      // of [0, N): SwiGLU gate columns, then up columns
-  const bool in = col < p.N;                        // (N is a multiple of 8)
-  float sum[8];
+  const int col = blockIdx.y * 256 + 8 * lane;      // of dy's columns (a multiple of 8)
+  float sum[H][8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) sum[k] = 0.f;
-  if (in) {
-    for (int r = r0 + warp; r < r0 + n; r += 8) {
-      float o[8];
-      uint4 zv, dv;
-      if (FN == MOE_FN_SWIGLU) {
-        const int c = col < p.No ? col : col - p.No;
-        const uint4 gv = __ldg(reinterpret_cast<const uint4*>(p.z + (int64_t)r * p.N + c));
-        const uint4 uv = __ldg(reinterpret_cast<const uint4*>(p.z + (int64_t)r * p.N + p.No + c));
-        dv = __ldg(reinterpret_cast<const uint4*>(p.dy + (int64_t)r * p.ld_dy + c));
-        const uint16_t* g16 = reinterpret_cast<const uint16_t*>(&gv);
-        const uint16_t* u16 = reinterpret_cast<const uint16_t*>(&uv);
-        const uint16_t* d16 = reinterpret_cast<const uint16_t*>(&dv);
+  for (int h = 0; h < H; ++h)
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float g0 = from16r(g16[k], bf), u0 = from16r(u16[k], bf), d = from16r(d16[k], bf);
-          const float g = clamp_hi(g0, p.limit), u = clamp_both(u0, p.limit);
-          const float s = __fdividef(1.f, 1.f + __expf(-g));
-          if (col < p.No) o[k] = g0 > p.limit ? 0.f : d * u * s * (1.f + g * (1.f - s));
-          else o[k] = fabsf(u0) <= p.limit ? d * g * s : 0.f;
+    for (int k = 0; k < 8; ++k) sum[h][k] = 0.f;
+  if (col < p.No) {
+    for (int r = r0 + warp; r < r1; r += 16) {
+      uint4 dv[2], zv[2], uv[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = r + 8 * i;
+        if (row < r1) {
+          dv[i] = __ldg(reinterpret_cast<const uint4*>(p.dy + row * p.ld_dy + col));
+          if (FN != MOE_FN_NONE) zv[i] = __ldg(reinterpret_cast<const uint4*>(p.z + row * p.N + col));
+          if (H == 2) uv[i] = __ldg(reinterpret_cast<const uint4*>(p.z + row * p.N + p.No + col));
         }
-      } else {
-        dv = __ldg(reinterpret_cast<const uint4*>(p.dy + (int64_t)r * p.ld_dy + col));
-        if (FN != MOE_FN_NONE) zv = __ldg(reinterpret_cast<const uint4*>(p.z + (int64_t)r * p.N + col));
-        const uint16_t* d16 = reinterpret_cast<const uint16_t*>(&dv);
-        const uint16_t* z16 = reinterpret_cast<const uint16_t*>(&zv);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          o[k] = act_grad<FN>(FN != MOE_FN_NONE ? from16r(z16[k], bf) : 0.f, from16r(d16[k], bf));
-      }
-      if (FN != MOE_FN_NONE) {
-        uint4 ov;
-        uint16_t* o16 = reinterpret_cast<uint16_t*>(&ov);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) o16[k] = to16r(o[k], bf);
-        *reinterpret_cast<uint4*>(p.dz + (int64_t)r * p.N + col) = ov;
       }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] += o[k];
+      for (int i = 0; i < 2; ++i) {
+        const int64_t row = r + 8 * i;
+        if (row < r1) {
+          float dy[8], z[8], u[8], o[8], ou[8];
+          widen(dv[i], bf, dy);
+          if (FN != MOE_FN_NONE) widen(zv[i], bf, z);
+          if (H == 2) widen(uv[i], bf, u);
+          act_grad8<FN>(p, z, u, dy, o, ou);
+          if (FN != MOE_FN_NONE) *reinterpret_cast<uint4*>(p.dz + row * p.N + col) = narrow(o, bf);
+          if (H == 2) *reinterpret_cast<uint4*>(p.dz + row * p.N + p.No + col) = narrow(ou, bf);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            sum[0][k] += o[k];
+            if (H == 2) sum[H - 1][k] += ou[k];
+          }
+        }
+      }
     }
   }
   if (!p.partial) return;
+  for (int h = 0; h < H; ++h) {
+    if (h) __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 8; ++k) s_sum[warp][8 * lane + k] = sum[k];
-  __syncthreads();
-  const int c = blockIdx.y * 256 + threadIdx.x;
-  if (c < p.N) {
-    float v = 0.f;
+    for (int k = 0; k < 8; ++k) s_sum[warp][8 * lane + k] = h == 0 ? sum[0][k] : sum[H - 1][k];
+    __syncthreads();
+    const int c = blockIdx.y * 256 + threadIdx.x;
+    if (c < p.No) {
+      float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) v += s_sum[w][threadIdx.x];
-    p.partial[(int64_t)blockIdx.x * p.N + c] = v;
+      for (int w = 0; w < 8; ++w) v += s_sum[w][threadIdx.x];
+      p.partial[(int64_t)blockIdx.x * p.N + h * p.No + c] = v;
+    }
   }
 }
 
@@ -1385,7 +1431,7 @@ int launch_act_grad(const ActGradArgs& a) {
   p.db = a.db;
   p.status = a.status;
   p.chunks = (int)act_grad_chunks(a.rows, a.offsets ? a.E : 1);
-  const dim3 grid((unsigned)p.chunks, (unsigned)((a.N + 255) / 256));
+  const dim3 grid((unsigned)p.chunks, (unsigned)((p.No + 255) / 256));
   auto kern = act_grad_kernel<MOE_FN_NONE>;
   switch (a.fn) {
     case MOE_FN_RELU: kern = act_grad_kernel<MOE_FN_RELU>; break;
