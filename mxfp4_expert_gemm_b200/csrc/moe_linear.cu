@@ -319,22 +319,38 @@ __device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable
 __device__ __forceinline__ int tail_shift(int n) { return n < kBK ? n - kBK : 0; }
 
 // ------------------------------------------------------------------------------ epilogue
-// Four warps (128 threads, named barrier `bar`) finish 32 columns of a tile: thread `row` holds
-// the fp32 values of TMEM lane `row` (column col0 + c in v[c]).  Lanes run along an output row,
-// so the 16-bit results pass through a [32][128] shared buffer and leave as 16-byte stores,
-// 256 bytes of an output row by 16 threads (64-byte stores straight from the lanes ran a weight
-// gradient's stores at 1.3 TB/s).
-// SwiGLU: lanes 0-63 hold the gate and lanes 64-127 the up values of the tile's 64 features; the
-// up lanes hand their values of columns 0-15 to the gate lanes, and take the gate values of
-// columns 16-31 from them, so that every thread finishes 16 columns.
-constexpr int kEpiBytes = 8192;
+// Four warps (128 threads, named barrier `bar`) finish 32 columns of a tile, held as matrix
+// fragments: warp q has TMEM lanes 32 q ..; value (h, g, r), index 16 h + 4 g + r, of lane l is
+// accumulator lane 32 q + 16 h + 8 (r / 2) + l / 4, column col0 + 8 g + 2 (l % 4) + r % 2.
+// Accumulator lanes run along an output row: the 16-bit results are transposed into a shared
+// buffer of output rows by stmatrix (8 x 8 values an instruction and matrix) and leave as 16-byte
+// stores, 256 bytes of an output row by 16 threads.  (A lane per row with 2-byte stores to shared
+// memory, 32 a thread, took 2.4 us of a 256 x 256 tile; with 2-byte stores to global memory, 5.)
+// The buffer's rows are padded by 16 bytes, so that the 8 pieces of a matrix fall on other banks.
+// SwiGLU: lanes 0-63 hold the gate and lanes 64-127 the up values of the tile's 64 features, the
+// same fragment positions in warps q and q + 2.  The up warps hand their values of columns 0-15
+// over, and take the gate values of columns 16-31, so that every thread finishes 16 columns.
+constexpr int kEpiBytes = 9216;
+constexpr int kPitch = 272, kPitchSw = 144;   // bytes per output row in the buffer: 128 or 64 values + 16
 
 __device__ __forceinline__ void group_sync(int bar) { asm volatile("bar.sync %0, 128;" ::"r"(bar) : "memory"); }
 
-// Rows c < n of a [32][W] 16-bit buffer to dst (row c at dst + c ld), columns < lim.
+// 32 accumulator columns of this warp's lanes as fragments (zeros where no contraction block was
+// added).  taddr: the warp's first lane and the first column.
+__device__ __forceinline__ void load_acc(uint32_t taddr, bool have, uint32_t (&v)[32]) {
+  ptx::tmem_ld_16x256b_x4(taddr, v);
+  ptx::tmem_ld_16x256b_x4(taddr + (16u << 16), v + 16);
+  ptx::tmem_wait_ld();
+  if (!have) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = 0u;
+  }
+}
+
+// Rows c < n of a buffer of W-value rows to dst (row c at dst + c ld), columns < lim.
 template <int W>
-__device__ __forceinline__ void store_rows(const LinParams& p, const uint8_t* buf, uint16_t* dst, int64_t ld, int n,
-                                           int lim, int th, const uint16_t* lo, const uint16_t* hi) {
+__device__ __forceinline__ void store_rows(const LinParams& p, const uint8_t* buf, int pitch, uint16_t* dst, int64_t ld,
+                                           int n, int lim, int th, const uint16_t* lo, const uint16_t* hi) {
   constexpr int V = W / 8;              // 16-byte pieces per row
   const int v = th % V;
   if (8 * v >= lim) return;             // (lim is a multiple of 8)
@@ -342,145 +358,173 @@ __device__ __forceinline__ void store_rows(const LinParams& p, const uint8_t* bu
   for (int c = th / V; c < 32; c += 128 / V) {
     if (c < n) {
       uint4* q = reinterpret_cast<uint4*>(dst + c * ld + 8 * v);
-      const uint4 val = *reinterpret_cast<const uint4*>(buf + c * (2 * W) + 16 * v);
+      const uint4 val = *reinterpret_cast<const uint4*>(buf + c * pitch + 16 * v);
       if (in_bounds(q, lo, hi, p.status)) *q = val;
     }
   }
 }
 
 template <int W>
-__device__ __forceinline__ void load_rows(uint8_t* buf, const uint16_t* src, int64_t ld, int n, int lim, int th) {
+__device__ __forceinline__ void load_rows(uint8_t* buf, int pitch, const uint16_t* src, int64_t ld, int n, int lim,
+                                          int th) {
   constexpr int V = W / 8;
   const int v = th % V;
   if (8 * v >= lim) return;
 #pragma unroll
   for (int c = th / V; c < 32; c += 128 / V)
-    if (c < n) *reinterpret_cast<uint4*>(buf + c * (2 * W) + 16 * v) = *reinterpret_cast<const uint4*>(src + c * ld + 8 * v);
+    if (c < n) *reinterpret_cast<uint4*>(buf + c * pitch + 16 * v) = *reinterpret_cast<const uint4*>(src + c * ld + 8 * v);
 }
 
-// 16-bit values of 32 columns into the buffer, each thread its lane's.
-template <bool BF>
-__device__ __forceinline__ void stage_lane(uint8_t* buf, const float (&v)[32], int row) {
-  uint16_t* b = reinterpret_cast<uint16_t*>(buf) + row;
+// Column groups G0 .. G0 + NG - 1 of the fragments into the buffer (row 8 g + k, this warp's 32
+// values at byte `at`), and back (added to v).
+template <bool BF, int G0, int NG>
+__device__ __forceinline__ void stage_frag(uint8_t* buf, int pitch, int at, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = ptx::smem_u32(buf) + (lane & 7) * pitch + at + 16 * (lane >> 3);
 #pragma unroll
-  for (int c = 0; c < 32; c += 2) {
-    const uint32_t w = to16x2<BF>(v[c], v[c + 1]);
-    b[c * 128] = (uint16_t)w;
-    b[(c + 1) * 128] = (uint16_t)(w >> 16);
+  for (int g = G0; g < G0 + NG; ++g)
+    ptx::stmatrix_x4_trans(base + 8 * g * pitch, to16x2<BF>(v[4 * g], v[4 * g + 1]),
+                           to16x2<BF>(v[4 * g + 2], v[4 * g + 3]), to16x2<BF>(v[16 + 4 * g], v[16 + 4 * g + 1]),
+                           to16x2<BF>(v[16 + 4 * g + 2], v[16 + 4 * g + 3]));
+}
+template <bool BF, int G0, int NG>
+__device__ __forceinline__ void add_frag(const uint8_t* buf, int pitch, int at, float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t base = ptx::smem_u32(buf) + (lane & 7) * pitch + at + 16 * (lane >> 3);
+#pragma unroll
+  for (int g = G0; g < G0 + NG; ++g) {
+    uint32_t w[4];
+    ptx::ldmatrix_x4_trans(base + 8 * g * pitch, w);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int i = 16 * (m >> 1) + 4 * g + 2 * (m & 1);
+      v[i] += from16<BF>((uint16_t)w[m]);
+      v[i + 1] += from16<BF>((uint16_t)(w[m] >> 16));
+    }
+  }
+}
+
+// SwiGLU of this thread's half of the columns (G0 = 0: gate warps, 2: up warps).
+template <bool BF, int G0>
+__device__ __forceinline__ void swiglu_half(const LinParams& p, float (&v)[32], const float4* theirs, int bar) {
+  constexpr bool UP = G0 == 2;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {   // piece k: (h, g) = (k / 2, G0 + k % 2)
+    const float4 o = theirs[64 * k];
+    const int i = 16 * (k >> 1) + 4 * (G0 + (k & 1));
+    const float other[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      v[i + r] = UP ? swiglu(other[r], v[i + r], p.limit) : swiglu(v[i + r], other[r], p.limit);
   }
 }
 
 template <int FN, bool BF>
-__device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t, float (&v)[32], int col0, int row,
+__device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t, float (&v)[32], int col0, int th,
                                             uint8_t* buf, int bar) {
   const int n = min(32, t.nj - col0);   // valid columns
   const int64_t r0 = t.j0 + col0;
   uint16_t* out = p.out + t.e * p.out_expert + r0 * p.ld_out + t.i0;
   const int lim = p.I - t.i0;           // columns of out from i0 on
+  const int q = th >> 5;
   group_sync(bar);                      // the buffer's last readers are done
   if (p.z) {
-    stage_lane<BF>(buf, v, row);
+    stage_frag<BF, 0, 4>(buf, kPitch, 64 * q, v);
     group_sync(bar);
-    if (FN == MOE_FN_SWIGLU) {
+    if (FN == MOE_FN_SWIGLU) {   // gate lanes' 64 columns to z's first half, up lanes' to its second
       const int64_t ldz = 2 * (int64_t)p.I;
-      // gate lanes' 64 columns to z's first half, up lanes' to its second
-      const int h = row >> 6;
-      const uint8_t* hb = buf + 128 * h;
+      const int h = th >> 6, w = th & 63, vv = w & 7;
       uint16_t* dst = p.z + r0 * ldz + h * (int64_t)p.I + t.i0;
-      const int w = row & 63, vv = w & 7;
       if (8 * vv < lim) {
 #pragma unroll
         for (int c = w >> 3; c < 32; c += 8)
           if (c < n) {
-            uint4* q = reinterpret_cast<uint4*>(dst + c * ldz + 8 * vv);
-            if (in_bounds(q, p.z, p.z_end, p.status)) *q = *reinterpret_cast<const uint4*>(hb + c * 256 + 16 * vv);
+            uint4* d = reinterpret_cast<uint4*>(dst + c * ldz + 8 * vv);
+            const uint4 val = *reinterpret_cast<const uint4*>(buf + c * kPitch + 128 * h + 16 * vv);
+            if (in_bounds(d, p.z, p.z_end, p.status)) *d = val;
           }
       }
     } else {
-      store_rows<128>(p, buf, p.z + r0 * p.I + t.i0, p.I, n, lim, row, p.z, p.z_end);
+      store_rows<128>(p, buf, kPitch, p.z + r0 * p.I + t.i0, p.I, n, lim, th, p.z, p.z_end);
     }
     group_sync(bar);
   }
   if (FN == MOE_FN_SWIGLU) {
-    const bool up = row >= 64;
-    const int f = row & 63;
-    float* ex = reinterpret_cast<float*>(buf);   // [2][16][64]: u of columns 0-15, g of columns 16-31
+    const bool up = q >= 2;
+    float4* ex = reinterpret_cast<float4*>(buf);   // [2][4][64] pieces: u of columns 0-15, g of columns 16-31
+    float4* mine = ex + (up ? 0 : 256) + (th & 63);
+    const float4* theirs = ex + (up ? 256 : 0) + (th & 63);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) ex[((up ? 0 : 16) + c) * 64 + f] = up ? v[c] : v[16 + c];
-    group_sync(bar);
-    float y[16];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const float o = ex[((up ? 16 : 0) + c) * 64 + f];
-      y[c] = up ? swiglu(o, v[16 + c], p.limit) : swiglu(v[c], o, p.limit);
+    for (int k = 0; k < 4; ++k) {
+      const int a = 16 * (k >> 1) + 4 * (k & 1), b = a + 8;   // column groups k % 2 and 2 + k % 2
+      mine[64 * k] = up ? make_float4(v[a], v[a + 1], v[a + 2], v[a + 3])
+                        : make_float4(v[b], v[b + 1], v[b + 2], v[b + 3]);
     }
     group_sync(bar);
-    uint16_t* b = reinterpret_cast<uint16_t*>(buf) + (up ? 16 * 64 : 0) + f;
+    if (up) swiglu_half<BF, 2>(p, v, theirs, bar);
+    else swiglu_half<BF, 0>(p, v, theirs, bar);
+    group_sync(bar);
+    const int at = 64 * (q & 1);
     if (p.residual) {
-      load_rows<64>(buf + 4096, p.residual + r0 * p.ld_res + t.i0, p.ld_res, n, lim, row);
+      load_rows<64>(buf + 32 * kPitchSw, kPitchSw, p.residual + r0 * p.ld_res + t.i0, p.ld_res, n, lim, th);
       group_sync(bar);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) y[c] += from16<BF>(b[2048 + c * 64]);
+      if (up) add_frag<BF, 2, 2>(buf + 32 * kPitchSw, kPitchSw, at, v);
+      else add_frag<BF, 0, 2>(buf + 32 * kPitchSw, kPitchSw, at, v);
     }
-#pragma unroll
-    for (int c = 0; c < 16; c += 2) {
-      const uint32_t w = to16x2<BF>(y[c], y[c + 1]);
-      b[c * 64] = (uint16_t)w;
-      b[(c + 1) * 64] = (uint16_t)(w >> 16);
-    }
+    if (up) stage_frag<BF, 2, 2>(buf, kPitchSw, at, v);
+    else stage_frag<BF, 0, 2>(buf, kPitchSw, at, v);
     group_sync(bar);
-    store_rows<64>(p, buf, out, p.ld_out, n, lim, row, p.out, p.out_end);
+    store_rows<64>(p, buf, kPitchSw, out, p.ld_out, n, lim, th, p.out, p.out_end);
   } else {
 #pragma unroll
     for (int c = 0; c < 32; ++c) v[c] = act_fn<FN>(v[c]);
     if (p.residual) {
-      load_rows<128>(buf, p.residual + r0 * p.ld_res + t.i0, p.ld_res, n, lim, row);
+      load_rows<128>(buf, kPitch, p.residual + r0 * p.ld_res + t.i0, p.ld_res, n, lim, th);
       group_sync(bar);
-      const uint16_t* b = reinterpret_cast<const uint16_t*>(buf) + row;
-#pragma unroll
-      for (int c = 0; c < 32; ++c) v[c] += from16<BF>(b[c * 128]);   // (read, then overwritten, by this thread alone)
+      add_frag<BF, 0, 4>(buf, kPitch, 64 * q, v);   // (a warp reads and then overwrites its own values alone)
+      __syncwarp();
     }
-    stage_lane<BF>(buf, v, row);
+    stage_frag<BF, 0, 4>(buf, kPitch, 64 * q, v);
     group_sync(bar);
-    store_rows<128>(p, buf, out, p.ld_out, n, lim, row, p.out, p.out_end);
+    store_rows<128>(p, buf, kPitch, out, p.ld_out, n, lim, th, p.out, p.out_end);
   }
 }
 
-// acc: the raw accumulator values; bias: this lane's.
+// acc: the raw accumulator values; bias: of this thread's four accumulator lanes; th: the thread's
+// number in its group, 32 q + lane.
 template <int MODE, bool SW, bool BF>
-__device__ __forceinline__ void finish(const LinParams& p, const LinTile& t, const uint32_t (&acc)[32], float bias,
-                                       int col0, int row, uint8_t* buf, int bar) {
+__device__ __forceinline__ void finish(const LinParams& p, const LinTile& t, const uint32_t (&acc)[32],
+                                       const float (&bias)[4], int col0, int th, uint8_t* buf, int bar) {
   if (col0 >= t.nj) return;   // (the same for the whole group)
   float v[32];
 #pragma unroll
-  for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(acc[c]) + bias;
-  if (SW) return finish_cols<MOE_FN_SWIGLU, BF>(p, t, v, col0, row, buf, bar);
+  for (int c = 0; c < 32; ++c) {
+    v[c] = __uint_as_float(acc[c]);
+    if (MODE == kForward) v[c] += bias[2 * (c >> 4) + ((c >> 1) & 1)];
+  }
+  if (SW) return finish_cols<MOE_FN_SWIGLU, BF>(p, t, v, col0, th, buf, bar);
   if (MODE == kForward) {
     switch (p.fn) {
-      case MOE_FN_RELU: return finish_cols<MOE_FN_RELU, BF>(p, t, v, col0, row, buf, bar);
-      case MOE_FN_GELU: return finish_cols<MOE_FN_GELU, BF>(p, t, v, col0, row, buf, bar);
-      case MOE_FN_GELU_TANH: return finish_cols<MOE_FN_GELU_TANH, BF>(p, t, v, col0, row, buf, bar);
-      case MOE_FN_SILU: return finish_cols<MOE_FN_SILU, BF>(p, t, v, col0, row, buf, bar);
+      case MOE_FN_RELU: return finish_cols<MOE_FN_RELU, BF>(p, t, v, col0, th, buf, bar);
+      case MOE_FN_GELU: return finish_cols<MOE_FN_GELU, BF>(p, t, v, col0, th, buf, bar);
+      case MOE_FN_GELU_TANH: return finish_cols<MOE_FN_GELU_TANH, BF>(p, t, v, col0, th, buf, bar);
+      case MOE_FN_SILU: return finish_cols<MOE_FN_SILU, BF>(p, t, v, col0, th, buf, bar);
     }
   }
-  finish_cols<MOE_FN_NONE, BF>(p, t, v, col0, row, buf, bar);
+  finish_cols<MOE_FN_NONE, BF>(p, t, v, col0, th, buf, bar);
 }
 
-// This lane's bias (SwiGLU: lanes 0-63 the gate's, 64-127 the up's).
+// The biases of this thread's accumulator lanes (SwiGLU: lanes 0-63 the gate's, 64-127 the up's).
 template <int MODE, bool SW>
-__device__ __forceinline__ float lane_bias(const LinParams& p, const LinTile& t, int row) {
-  if (MODE != kForward || !p.bias) return 0.f;
-  const int i = t.i0 + (SW ? row & 63 : row);
-  return i < p.I ? __ldg(p.bias + (int64_t)t.e * p.a_rows + (SW && row >= 64 ? p.I : 0) + i) : 0.f;
-}
-
-// 32 accumulator columns of this warp's lanes (zeros where no contraction block was added).
-__device__ __forceinline__ void load_acc(uint32_t taddr, bool have, uint32_t (&v)[32]) {
-  ptx::tmem_ld32(taddr, v);
-  ptx::tmem_wait_ld();
-  if (!have) {
+__device__ __forceinline__ void lane_bias(const LinParams& p, const LinTile& t, int th, float (&bias)[4]) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = 0u;
+  for (int k = 0; k < 4; ++k) {
+    bias[k] = 0.f;
+    if (MODE == kForward && p.bias) {
+      const int row = 32 * (th >> 5) + 8 * k + ((th & 31) >> 2);
+      const int i = t.i0 + (SW ? row & 63 : row);
+      if (i < p.I) bias[k] = __ldg(p.bias + (int64_t)t.e * p.a_rows + (SW && row >= 64 ? p.I : 0) + i);
+    }
   }
 }
 
@@ -497,10 +541,10 @@ struct SplitCfg {
   static constexpr int CPS = 2;                         // CTAs per SM
   static constexpr int S = 108 * 1024 / STAGE;
   static constexpr int TMEM_COLS = NB;
-  // The stages are reused: the tile's fp32 partials, the received ones ([splits][ceil(nw /
-  // splits)][128]), the epilogue's buffer.  128-wide tiles leave no room for the first two.
+  // The stages are reused: the tile's fp32 partials, the received ones (splits x whole groups of
+  // 8 columns: at most 7 more columns per split), the epilogue's buffer.  128-wide tiles leave no room for the first two.
   static constexpr bool SPLIT = NB <= 64;
-  static constexpr int SEND_BYTES = SPLIT ? NB * 512 : 0, RED_BYTES = SPLIT ? (NB + 8) * 512 : 0;
+  static constexpr int SEND_BYTES = SPLIT ? NB * 512 : 0, RED_BYTES = SPLIT ? (NB + 32) * 512 : 0;
   static constexpr int EPI_OFF = SEND_BYTES + RED_BYTES;
   static constexpr int BAR_BYTES = 8 * (2 * S + 3) + 64;
   static constexpr int SMEM = S * STAGE + BAR_BYTES + 1024 /* align slack */;
@@ -649,7 +693,8 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
     const bool ready = ptx::mbar_wait_bounded(accf, 0, s_abort, kWaitNs);
     if (!ptx::bar_or<1, 128>(!ready) && t.ok) {
       ptx::tc_fence_after();
-      const float bias = lane_bias<MODE, SW>(p, t, row);
+      float bias[4];
+      lane_bias<MODE, SW>(p, t, row, bias);
       if (S == 1) {
         for (int c0 = 0; c0 < t.nw; c0 += 32) {
           uint32_t v[32];
@@ -668,17 +713,24 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
     // threads took up to 30 us here).  The sum runs in rank order, so that it does not depend
     // on timing.
     const int row = 32 * (warp & 3) + lane;
-    const int per = (t.nw + S - 1) / S;   // columns per CTA
-    auto share = [&](int r) { return max(0, min((r + 1) * per, t.nj) - r * per); };   // valid columns of CTA r
-    float* src = reinterpret_cast<float*>(smem);                       // [nw][128]
-    float* dst = reinterpret_cast<float*>(smem + C::SEND_BYTES);       // [S][per][128]
+    const int per = ((t.nw + S - 1) / S + 7) / 8 * 8;   // columns per CTA, in groups of 8
+    auto share = [&](int r) { return max(0, min((r + 1) * per, (t.nj + 7) / 8 * 8) - r * per); };   // columns of CTA r
+    // partials by column group and thread, 8 fragment values each: [nw / 8][2][128] and
+    // [S][per / 8][2][128] pieces of 16 bytes
+    float4* src = reinterpret_cast<float4*>(smem);
+    float4* dst = reinterpret_cast<float4*>(smem + C::SEND_BYTES);
     if (warp >= 2 && t.ok) {
       const uint32_t acc = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
       for (int c0 = 0; c0 < t.nj; c0 += 32) {
         uint32_t v[32];
         load_acc(acc + c0, kb1 > kb0, v);
+        const float* f = reinterpret_cast<const float*>(v);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) src[(c0 + c) * 128 + row] = __uint_as_float(v[c]);
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            src[((c0 / 8 + g) * 2 + h) * 128 + row] = make_float4(f[16 * h + 4 * g], f[16 * h + 4 * g + 1],
+                                                                f[16 * h + 4 * g + 2], f[16 * h + 4 * g + 3]);
       }
       ptx::fence_proxy_async_smem();   // the copies read what the threads wrote
     }
@@ -689,7 +741,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
         for (int r = 0; r < S; ++r) {
           const int n = share(r);
           if (n > 0)
-            ptx::bulk_copy_cluster(ptx::mapa_shared(dst + rank * per * 128, r), src + r * per * 128, (uint32_t)n * 512,
+            ptx::bulk_copy_cluster(ptx::mapa_shared(dst + rank * per * 32, r), src + r * per * 32, (uint32_t)n * 512,
                                    ptx::mapa_shared(redf, r));
         }
       }
@@ -698,11 +750,11 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
     if (warp >= 2 && t.ok) {
       const bool here = ptx::mbar_wait_cluster_bounded(redf, 0, s_abort, kWaitNs);
       if (!ptx::bar_or<1, 128>(!here)) {
-        const float bias = lane_bias<MODE, SW>(p, t, row);
+        float bias[4];
+        lane_bias<MODE, SW>(p, t, row, bias);
         const int c1 = min((rank + 1) * per, t.nj);
         LinTile part = t;
         part.nj = c1;
-        const float* red = dst + row;
         for (int c0 = rank * per; c0 < c1; c0 += 32) {
           // One rank's 32 columns at a time, in straight-line code: a loop over the ranks inside
           // each column ran cold instructions column by column, 17 us for 32 of them.  Columns past
@@ -713,9 +765,16 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
           for (int c = 0; c < 32; ++c) sum[c] = 0.f;
 #pragma unroll 1
           for (int r = 0; r < S; ++r) {
-            const float* q = red + (r * per + c0 - rank * per) * 128;
+            const float4* q = dst + ((r * per + c0 - rank * per) / 8) * 256 + row;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) sum[c] += q[c * 128];
+            for (int k = 0; k < 8; ++k) {   // (g, h) = (k / 2, k % 2)
+              const float4 w = q[k * 128];
+              const int i = 16 * (k & 1) + 4 * (k >> 1);
+              sum[i] += w.x;
+              sum[i + 1] += w.y;
+              sum[i + 2] += w.z;
+              sum[i + 3] += w.w;
+            }
           }
 #pragma unroll
           for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(sum[c]);
@@ -927,7 +986,8 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       t.i0 += kIW / 2 * rank;
       const int b2 = li & 1;
       const bool have = t.clen > 0;
-      const float bias = lane_bias<MODE, SW>(p, t, row);
+      float bias[4];
+      lane_bias<MODE, SW>(p, t, row, bias);
       const bool ready = !*s_abort && ptx::mbar_wait_bounded(&accf[b2], (uint32_t)(li >> 1) & 1, s_abort, kWaitNs);
       // (one answer for all epilogue warps: another role may raise the abort flag at any time)
       if (ptx::bar_or<1, 32 * C::EPI_WARPS>(!ready)) break;
@@ -941,13 +1001,8 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       if (32 * part >= t.nw) release();
       for (int c0 = 32 * part; c0 < t.nw; c0 += 64) {
         uint32_t v[32];
-        ptx::tmem_ld32(acc + c0, v);
-        ptx::tmem_wait_ld();
+        load_acc(acc + c0, have, v);   // (an expert without rows: never written)
         if (c0 + 64 >= t.nw) release();
-        if (!have) {   // an expert without rows: the accumulator was never written
-#pragma unroll
-          for (int c = 0; c < 32; ++c) v[c] = 0u;
-        }
         finish<MODE, SW, BF>(p, t, v, bias, c0, row, epi + kEpiBytes * part, 2 + part);
       }
     }
