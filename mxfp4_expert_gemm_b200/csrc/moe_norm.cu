@@ -29,9 +29,9 @@ __device__ __forceinline__ uint16_t store1(float v, BF16) { return __bfloat16_as
 __device__ __forceinline__ uint16_t store1(float v, FP16) { return __half_as_ushort(__float2half_rn(v)); }
 __device__ __forceinline__ float store1(float v, FP32) { return v; }
 
-// VEC consecutive values, as stored (16 bytes, or one value).
+// VEC consecutive values, as stored: 16 bytes, or 4 (two 16-bit values), or one value.
 template <class DT, int VEC>
-struct alignas(VEC == 1 ? sizeof(typename DT::Store) : 16) Pack {
+struct alignas(VEC * sizeof(typename DT::Store)) Pack {
   typename DT::Store v[VEC];
 };
 
@@ -47,11 +47,16 @@ __device__ __forceinline__ void store_pack(void* base, int64_t at, const Pack<DT
 // A pack's values in fp32 and back: two 16-bit values per 32-bit word.
 template <class DT, int VEC>
 __device__ __forceinline__ void unpack(const Pack<DT, VEC>& p, float (&f)[VEC]) {
-  if constexpr (VEC == 8) {
-    const uint4 q = *reinterpret_cast<const uint4*>(&p);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  if constexpr (VEC > 1 && sizeof(typename DT::Store) == 2) {
+    uint32_t w[VEC / 2];
+    if constexpr (VEC == 8) {
+      const uint4 q = *reinterpret_cast<const uint4*>(&p);
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    } else {
+      w[0] = *reinterpret_cast<const uint32_t*>(&p);
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < VEC / 2; ++i) {
       if constexpr (std::is_same<DT, BF16>::value) {
         f[2 * i] = __uint_as_float(w[i] << 16);
         f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
@@ -69,10 +74,10 @@ __device__ __forceinline__ void unpack(const Pack<DT, VEC>& p, float (&f)[VEC]) 
 template <class DT, int VEC>
 __device__ __forceinline__ Pack<DT, VEC> pack(const float (&f)[VEC]) {
   Pack<DT, VEC> p;
-  if constexpr (VEC == 8) {
-    uint32_t w[4];
+  if constexpr (VEC > 1 && sizeof(typename DT::Store) == 2) {
+    uint32_t w[VEC / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < VEC / 2; ++i) {
       if constexpr (std::is_same<DT, BF16>::value) {
         const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t*>(&v);
@@ -81,7 +86,8 @@ __device__ __forceinline__ Pack<DT, VEC> pack(const float (&f)[VEC]) {
         w[i] = *reinterpret_cast<const uint32_t*>(&v);
       }
     }
-    *reinterpret_cast<uint4*>(&p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (VEC == 8) *reinterpret_cast<uint4*>(&p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint32_t*>(&p) = w[0];
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) p.v[j] = store1(f[j], DT{});
@@ -232,8 +238,9 @@ struct NormParams {
 // VEC consecutive fp32 values (the packs of w, b and the column sums).
 template <int VEC>
 __device__ __forceinline__ void load_f32(const float* base, int at, float (&v)[VEC]) {
-  if (VEC == 1) {
-    v[0] = __ldg(base + at);
+  if constexpr (VEC <= 2) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = __ldg(base + at + j);
   } else {
 #pragma unroll
     for (int j = 0; j < VEC; j += 4) {
@@ -423,7 +430,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
 // D > 0: rows come through a D-deep ring of asynchronous copies into each thread's own slots, and
 // are read from there twice, which keeps the registers for the sums.  D = 0: loaded in place.
 template <class DT, int VEC, int NV, int R, int D, bool LAYER>
-__global__ void __launch_bounds__(576) norm_backward_kernel(const NormParams p) {
+__global__ void __launch_bounds__(VEC < 4 ? 1024 : 576) norm_backward_kernel(const NormParams p) {
   __shared__ __align__(16) float s_red[2 * R * 32];
   extern __shared__ float4 s_dyn[];   // the ring, then the block's column sums (2 d floats)
   const int threads = blockDim.x * blockDim.y, self = threadIdx.y * blockDim.x + threadIdx.x;
@@ -704,14 +711,14 @@ NormParams params_of(const NormArgs& a) {
   return p;
 }
 
-bool vec_ok(const void* q, int64_t ld, int vec, int size) {
-  return !q || ((reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld % vec == 0 && vec * size == 16);
+bool vec_ok(const void* q, int64_t ld, int vec, int bytes) {
+  return !q || ((reinterpret_cast<uintptr_t>(q) & (bytes - 1)) == 0 && ld % vec == 0);
 }
 
-// A row's threads: whole warps, at most `nv` packs each; more than 512: 0 (the row is long).
-int row_threads(int packs, int nv) {
+// A row's threads: whole warps, at most `nv` packs each; more than `most`: 0 (the row is long).
+int row_threads(int packs, int nv, int most = 512) {
   const int t = ((packs + nv - 1) / nv + 31) / 32 * 32;
-  return t <= 512 ? t : 0;
+  return t <= most ? t : 0;
 }
 
 template <class K>
@@ -723,22 +730,24 @@ bool allow_smem(K kern, size_t bytes) {
 template <class DT, int VEC, bool LAYER>
 int forward_vec(const NormArgs& a) {
   const NormParams p = params_of(a);
-  const int packs = a.d / VEC;
+  const int packs = a.d / VEC, lane = (packs + 31) / 32;   // packs a lane
   void (*kern)(NormParams) = nullptr;
   dim3 grid, block;
-  // A warp per row where the row fits a warp's registers (at most 12 packs a lane) and the rows
-  // are many; few rows are spread over blocks (16 x 2880: 2.2 us against 3 us).
-  if (a.T >= 2 * multiprocessors() && packs <= 32 * 12) {
-    kern = packs <= 64    ? norm_warp_kernel<DT, VEC, 2, LAYER>
-           : packs <= 128 ? norm_warp_kernel<DT, VEC, 4, LAYER>
-           : packs <= 256 ? norm_warp_kernel<DT, VEC, 8, LAYER>
-                          : norm_warp_kernel<DT, VEC, 12, LAYER>;
+  // A warp per row where the row fits a warp's registers (96 values a lane, 48 where each takes a
+  // register of its own) and the rows are many; few rows are spread over blocks (16 x 2880: 2.2 us
+  // against 3 us).
+  constexpr int U = VEC == 1 ? 6 : VEC == 2 ? 8 : VEC == 4 ? 2 : 2;   // packs a lane in steps of U, 2 U, 4 U, 6 U
+  if (a.T >= 2 * multiprocessors() && lane <= 6 * U) {
+    kern = lane <= U       ? norm_warp_kernel<DT, VEC, U, LAYER>
+           : lane <= 2 * U ? norm_warp_kernel<DT, VEC, 2 * U, LAYER>
+           : lane <= 4 * U ? norm_warp_kernel<DT, VEC, 4 * U, LAYER>
+                           : norm_warp_kernel<DT, VEC, 6 * U, LAYER>;
     grid = dim3((unsigned)((a.T + 3) / 4));
     block = dim3(128);
   } else {
-    constexpr int NV = VEC == 1 ? 16 : 4;
-    const int g1 = row_threads(packs, 1), g = g1 ? g1 : row_threads(packs, NV);
-    kern = g1 ? norm_block_kernel<DT, VEC, 1, LAYER>
+    constexpr int NV = 32 / VEC < 16 ? 32 / VEC : 16, N1 = VEC >= 4 ? 1 : 4;
+    const int g1 = row_threads(packs, N1), g = g1 ? g1 : row_threads(packs, NV);
+    kern = g1 ? norm_block_kernel<DT, VEC, N1, LAYER>
            : g ? norm_block_kernel<DT, VEC, NV, LAYER> : norm_long_kernel<DT, VEC, LAYER>;
     grid = dim3((unsigned)a.T);
     block = dim3(g ? g : 1024);
@@ -748,16 +757,20 @@ int forward_vec(const NormArgs& a) {
 
 template <class DT, int VEC, bool LAYER>
 int backward_vec(const NormArgs& a) {
-  // Two packs a thread: half the warps of one pack, which each repeat a row's reductions.
-  constexpr int NV = VEC == 1 ? 8 : 2, R = VEC == 1 ? 1 : 2, D = VEC == 1 ? 0 : 2;
+  // 16-byte packs: two a thread (a row on half the warps, which each repeat its reductions) and
+  // copies ahead.  Pairs and single values: eight values a thread, loaded in place, and as many
+  // threads as the registers allow instead.
+  constexpr int NV = VEC >= 4 ? 2 : 8 / VEC, R = VEC < 4 ? 1 : 2, D = VEC < 4 ? 0 : 2, most = VEC < 4 ? 1024 : 512;
   NormParams p = params_of(a);
-  const int g = row_threads(a.d / VEC, NV);
+  const int g = row_threads(a.d / VEC, NV, most);
   int n = 1;
   if (g) {
     const int y = g == 32 ? 8 : 1;   // short rows: a warp each, eight groups to a block
-    // several rows at a time, and copies ahead, once every resident block has several to take
-    const bool many = a.T >= 8 * multiprocessors() * y;
-    const int64_t fit = (int64_t)multiprocessors() * std::max(1, 576 / (g * y)), rows = y * (many ? R : 1);
+    // several rows at a time, and copies ahead, once every resident block has eight steps to take
+    // (the larger code is cold until then; copies of 4 bytes ran slower than loads)
+    const int64_t fit = (int64_t)multiprocessors() * std::max(1, (VEC < 4 ? 1024 : 576) / (g * y));
+    const bool many = D > 0 && a.T >= 8 * R * fit * y;
+    const int64_t rows = y * (many ? R : 1);
     p.blocks = (int)std::min(std::min<int64_t>((a.T + rows - 1) / rows, fit), norm_partial_rows(a.T, a.d));
     const size_t smem = (many ? (size_t)D * R * NV * 3 * 16 * g * y : 0) + (y > 1 ? 8 * (size_t)a.d : 0);
     auto kern = many ? norm_backward_kernel<DT, VEC, NV, R, D, LAYER> : norm_backward_kernel<DT, VEC, NV, 1, 0, LAYER>;
@@ -783,14 +796,28 @@ int backward_vec(const NormArgs& a) {
   return n + 1;
 }
 
+// Whether every row of the call is whole packs of VEC values at their alignment.
+template <class DT, int VEC>
+bool packs_ok(const NormArgs& a) {
+  constexpr int bytes = VEC * (int)sizeof(typename DT::Store);
+  return a.d % VEC == 0 && vec_ok(a.x, a.ldx, VEC, bytes) && vec_ok(a.y, a.ldy, VEC, bytes) &&
+         vec_ok(a.dy, a.lddy, VEC, bytes) && vec_ok(a.dres, a.lddres, VEC, bytes) &&
+         vec_ok(a.dx, a.lddx, VEC, bytes) && (VEC < 4 || (vec_ok(a.w, 4, 4, 16) && vec_ok(a.b, 4, 4, 16)));
+}
+
+template <class DT, int VEC, bool LAYER>
+int run_vec(const NormArgs& a, bool backward) {
+  return backward ? backward_vec<DT, VEC, LAYER>(a) : forward_vec<DT, VEC, LAYER>(a);
+}
+
 template <class DT, bool LAYER>
 int dispatch_vec(const NormArgs& a, bool backward) {
-  constexpr int size = sizeof(typename DT::Store), VEC = 16 / size;
-  const bool v = a.d % VEC == 0 && vec_ok(a.x, a.ldx, VEC, size) && vec_ok(a.y, a.ldy, VEC, size) &&
-                 vec_ok(a.dy, a.lddy, VEC, size) && vec_ok(a.dres, a.lddres, VEC, size) &&
-                 vec_ok(a.dx, a.lddx, VEC, size) && vec_ok(a.w, VEC, VEC, size) && vec_ok(a.b, VEC, VEC, size);
-  if (backward) return v ? backward_vec<DT, VEC, LAYER>(a) : backward_vec<DT, 1, LAYER>(a);
-  return v ? forward_vec<DT, VEC, LAYER>(a) : forward_vec<DT, 1, LAYER>(a);
+  constexpr int VEC = 16 / (int)sizeof(typename DT::Store);
+  if (packs_ok<DT, VEC>(a)) return run_vec<DT, VEC, LAYER>(a, backward);
+  if constexpr (VEC == 8) {   // 16-bit rows of even length: pairs
+    if (packs_ok<DT, 2>(a)) return run_vec<DT, 2, LAYER>(a, backward);
+  }
+  return run_vec<DT, 1, LAYER>(a, backward);
 }
 
 int dispatch(const NormArgs& a, bool backward) {
