@@ -542,13 +542,26 @@ def _status(status_word, dev):
     return None if status_word is None else _flat(status_word, torch.int32, "status_word", dev, status_word.shape)
 
 
-def _workspace(ws, nbytes, like, dev):
-    """(tensor, address, bytes) of a caller's workspace, or of one taken from torch's allocator."""
+def _workspace(ws, nbytes, like, dev, stream):
+    """(tensor, address, bytes) of a caller's workspace, or of one taken from torch's allocator (which
+    must not hand it on before a `stream` other than the current one has passed the call)."""
     if ws is None:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        ws = like.new_empty((nbytes + like.element_size() - 1) // like.element_size())
+        if stream is not None:
+            ws.record_stream(stream)
     elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
         raise ValueError(f"ws: a contiguous tensor on cuda:{dev} is required")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _rows_like(x, rows, cols):
+    """An output of x's type; torch's cheapest allocation where x's shape and strides are its own."""
+    return torch.empty_like(x) if x.is_contiguous() and x.shape[1] == cols else x.new_empty((rows, cols))
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_scratch(T: int, d: int) -> int:
+    return lib().moe_norm_workspace_bytes(T, d)
 
 
 def _norm_args(x, kind):
@@ -570,15 +583,16 @@ def moe_norm(x, w, b=None, kind="rms", eps=1e-5, y=None, want_stats=False, strea
     or fp32 rows, fp32 w and b.  With want_stats: (y, mean, rstd) for moe_norm_backward (mean is
     None for "rms")."""
     dev, dt, k, T, d, ldx = _norm_args(x, kind)
+    wp = _flat(w, torch.float32, "w", dev, (d,))
     if y is None:
-        y, ldy = x.new_empty((T, d)), d
+        y, ldy = _rows_like(x, T, d), d
     else:
         ldy = _rows(y, x.dtype, "y", dev, T, d)
     mean = rstd = None
     if want_stats:
-        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+        rstd = w.new_empty(T)
         mean = torch.empty_like(rstd) if k == 1 else None
-    _check((_lib or lib()).moe_norm(k, dt, T, d, x.data_ptr(), ldx, _flat(w, torch.float32, "w", dev, (d,)),
+    _check((_lib or lib()).moe_norm(k, dt, T, d, x.data_ptr(), ldx, wp,
                                     _flat(b, torch.float32, "b", dev, (d,)), eps, y.data_ptr(), ldy,
                                     None if mean is None else mean.data_ptr(),
                                     None if rstd is None else rstd.data_ptr(), _raw_stream(stream, dev)), "moe_norm")
@@ -599,17 +613,18 @@ def moe_norm_backward(dy, x, w, mean, rstd, kind="rms", dres=None, dx=None, need
         need_db = k == 1
     lddy = _rows(dy, x.dtype, "dy", dev, T, d)
     lddres = 0 if dres is None else _rows(dres, x.dtype, "dres", dev, T, d)
+    wp = _flat(w, torch.float32, "w", dev, (d,))
     if dx is None:
-        dx, lddx = x.new_empty((T, d)), d
+        dx, lddx = _rows_like(x, T, d), d
     else:
         lddx = _rows(dx, x.dtype, "dx", dev, T, d)
-    dw = torch.empty(d, dtype=torch.float32, device=x.device) if need_dw else None
-    db = torch.empty(d, dtype=torch.float32, device=x.device) if need_db else None
+    dw = torch.empty_like(w) if need_dw else None
+    db = torch.empty_like(w) if need_db else None
     ws_ptr, ws_bytes = None, 0
     if need_dw or need_db:
-        ws, ws_ptr, ws_bytes = _workspace(ws, moe_norm_workspace_bytes(T, d), x, dev)
+        ws, ws_ptr, ws_bytes = _workspace(ws, _norm_scratch(T, d), x, dev, stream)
     _check((_lib or lib()).moe_norm_backward(
-        k, dt, T, d, dy.data_ptr(), lddy, x.data_ptr(), ldx, _flat(w, torch.float32, "w", dev, (d,)),
+        k, dt, T, d, dy.data_ptr(), lddy, x.data_ptr(), ldx, wp,
         _flat(mean, torch.float32, "mean", dev, (T,)), _flat(rstd, torch.float32, "rstd", dev, (T,)),
         None if dres is None else dres.data_ptr(), lddres, dx.data_ptr(), lddx,
         None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), ws_ptr, ws_bytes,
@@ -629,6 +644,11 @@ def make_linear_dims(K: int, N: int, E: int = 1, dtype=torch.bfloat16, fn: str =
 
 def moe_linear_workspace_bytes(dims: moe_linear_dims, rows: int) -> int:
     return lib().moe_linear_workspace_bytes(ctypes.byref(dims), rows)
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_scratch(K, N, E, dtype, fn, limit, rows):
+    return moe_linear_workspace_bytes(make_linear_dims(K, N, E, dtype, fn, limit), rows)
 
 
 def _product_dims(x, w, grouped, fn, limit):
@@ -684,7 +704,7 @@ def _backward_product(what, dy, x, w, offsets, z, fn, limit, dx, dw, need_dx, ne
     if dx is not None:
         dxp, lddx = dx.data_ptr(), _rows(dx, x.dtype, "dx", dev, rows, K)
     elif need_dx:
-        dx, lddx = x.new_empty((rows, K)), K
+        dx, lddx = _rows_like(x, rows, K), K
         dxp = dx.data_ptr()
     if dw is not None:
         dwp = _flat(dw, x.dtype, "dw", dev, w.shape)
@@ -696,7 +716,7 @@ def _backward_product(what, dy, x, w, offsets, z, fn, limit, dx, dw, need_dx, ne
         dbp = db.data_ptr()
     ws_ptr, ws_bytes = None, 0
     if fn != "none" or need_db:
-        ws, ws_ptr, ws_bytes = _workspace(ws, moe_linear_workspace_bytes(dims, rows), x, dev)
+        ws, ws_ptr, ws_bytes = _workspace(ws, _linear_scratch(K, N, dims.E, x.dtype, fn, limit, rows), x, dev, stream)
     common = (zp, dxp, lddx, dwp, dbp, ws_ptr, ws_bytes, _status(status_word, dev), _raw_stream(stream, dev))
     L = _lib or lib()
     if grouped:

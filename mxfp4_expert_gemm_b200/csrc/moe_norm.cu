@@ -9,6 +9,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "moe_linear.cuh"
@@ -721,10 +722,16 @@ int row_threads(int packs, int nv, int most = 512) {
   return t <= most ? t : 0;
 }
 
+// The kernel's dynamic shared memory limit, raised to the most it can ask for once per device.
 template <class K>
-bool allow_smem(K kern, size_t bytes) {
-  return bytes <= 48 * 1024 ||
-         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+bool allow_smem(K kern, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return true;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024) != cudaSuccess) return false;
+  if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return true;
 }
 
 template <class DT, int VEC, bool LAYER>
@@ -774,7 +781,8 @@ int backward_vec(const NormArgs& a) {
     p.blocks = (int)std::min(std::min<int64_t>((a.T + rows - 1) / rows, fit), norm_partial_rows(a.T, a.d));
     const size_t smem = (many ? (size_t)D * R * NV * 3 * 16 * g * y : 0) + (y > 1 ? 8 * (size_t)a.d : 0);
     auto kern = many ? norm_backward_kernel<DT, VEC, NV, R, D, LAYER> : norm_backward_kernel<DT, VEC, NV, 1, 0, LAYER>;
-    if (!allow_smem(kern, smem)) return -1;
+    static std::atomic<uint64_t> done{0};
+    if (smem > 48 * 1024 && !allow_smem(norm_backward_kernel<DT, VEC, NV, R, D, LAYER>, done)) return -1;
     if (launch_kernel(kern, dim3((unsigned)p.blocks), dim3(g, y), smem, a.stream, false, p) != cudaSuccess) return -1;
   } else {
     p.blocks = (int)norm_partial_rows(a.T, a.d);

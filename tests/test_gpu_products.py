@@ -356,3 +356,72 @@ def test_injected_timeout_is_reported_and_cleared():
     assert moe.moe_device_status(st) == moe.MOE_ERR_TIMEOUT
     y = moe.moe_linear(x, w, status_word=st)
     assert moe.moe_device_status(st) == moe.MOE_OK and bool((y == 256).all())
+
+
+def test_on_a_stream_that_is_not_current():
+    """`stream=`: the call's own scratch stays with that stream until it has passed."""
+    g = generator(31)
+    M, K, N = 300, 256, 640
+    x, w, dy, z = normal(g, M, K), normal(g, N, K, std=0.1), normal(g, M, N // 2), normal(g, M, N)
+    want = moe.moe_linear_backward(dy, x, w, z, fn="swiglu", need_db=True)
+    s = torch.cuda.Stream()
+    for _ in range(20):
+        s.wait_stream(torch.cuda.current_stream())
+        got = moe.moe_linear_backward(dy, x, w, z, fn="swiglu", need_db=True, stream=s)
+        torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(255)   # would take the scratch's place
+        s.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    big = [torch.empty(50 * 1024 * 1024, dtype=torch.uint8, device="cuda")]   # a workspace of the caller's
+    got = moe.moe_linear_backward(dy, x, w, z, fn="swiglu", need_db=True, ws=big[0])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    with pytest.raises(moe.MoeError):
+        moe.moe_linear_backward(dy, x, w, z, fn="swiglu", ws=big[0][:4096])
+
+
+BAND = 4096   # bytes of canary on each side (keeps 16-byte alignment)
+
+
+def _banded(t):
+    """The tensor's values inside a larger buffer of canary bytes: (buffer, view)."""
+    n = t.numel() * t.element_size()
+    buf = torch.full((n + 2 * BAND,), 0xA5, dtype=torch.uint8, device="cuda")
+    view = buf[BAND:BAND + n].view(t.dtype).view(t.shape)
+    view.copy_(t)
+    return buf, view
+
+
+def _intact(buf):
+    return bool((buf[:BAND] == 0xA5).all()) and bool((buf[-BAND:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("counts,pad,first,K,N,fn,dt", [c for c in GROUPED if sum(c[0]) < 2000])
+def test_no_store_outside_the_outputs(counts, pad, first, K, N, fn, dt):
+    """Guard bands around every output and the workspace, and the bounds-checking build, whose
+    stores at computed addresses report one outside its buffer."""
+    from mxfp4_expert_gemm_b200 import build as libbuild
+    g, E, off, P, No, x, w, b = _grouped_case(counts, pad, first, K, N, fn, dt, seed=5)
+    dy, z, offd = normal(g, P, No, dtype=dt), normal(g, P, N, dtype=dt), off.cuda()
+    zz = z if fn != "none" else None
+    blank = lambda *s: torch.zeros(s, dtype=dt, device="cuda")  # noqa: E731
+    bufs = [_banded(t) for t in (blank(P, No), blank(P, N), blank(P, K), blank(E, N, K))]
+    (yb, y), (zb, zo), (dxb, dx), (dwb, dw) = bufs
+    dims = moe.make_linear_dims(K, N, E, dt, fn)
+    wsb, ws = _banded(torch.zeros(moe.moe_linear_workspace_bytes(dims, P), dtype=torch.uint8, device="cuda"))
+
+    def run():
+        st = _status()
+        moe.moe_grouped_linear(x, w, offd, b, fn=fn, y=y, z=zo, want_z=True, status_word=st)
+        moe.moe_grouped_linear_backward(dy, x, w, offd, zz, fn=fn, dx=dx, dw=dw, need_db=True, ws=ws, status_word=st)
+        _ok(st)
+        return [t.clone() for t in (y, zo, dx, dw)]
+
+    first_run = run()
+    assert all(_intact(t) for t in (yb, zb, dxb, dwb, wsb))
+    for t in (y, zo, dx, dw):
+        t.zero_()
+    with moe.use_library(libbuild.build(bounds=True)):
+        second = run()
+    for a, c in zip(first_run, second):
+        assert torch.equal(a, c)
