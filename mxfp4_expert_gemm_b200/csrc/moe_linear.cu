@@ -21,6 +21,7 @@
 
 #include "linear_ptx.cuh"
 #include "moe_linear.cuh"
+#include "packed_math.cuh"
 
 namespace moe {
 namespace {
@@ -87,23 +88,27 @@ __device__ __forceinline__ float from16(uint16_t v) {
 // accuracy where the left sides cancel.  erfc by the Chebyshev fit of Press et al., Numerical
 // Recipes, "erfcc" (relative error 1.2e-7 everywhere): one exponential and one divide, where erfcf
 // set the time of products with a short contraction (16336 x 144 x 4384: 340 us).
-__device__ __forceinline__ float normal_tail(float z) {   // erfc(|z| / sqrt 2) / 2
-  const float x = fabsf(z) * 0.70710678f;
-  const float t = __fdividef(1.f, fmaf(0.5f, x, 1.f));
-  float q = fmaf(t, 0.17087277f, -0.82215223f);
-  q = fmaf(t, q, 1.48851587f);
-  q = fmaf(t, q, -1.13520398f);
-  q = fmaf(t, q, 0.27886807f);
-  q = fmaf(t, q, -0.18628806f);
-  q = fmaf(t, q, 0.09678418f);
-  q = fmaf(t, q, 0.37409196f);
-  q = fmaf(t, q, 1.00002368f);
-  q = fmaf(t, q, -1.26551223f);
-  return 0.5f * t * __expf(fmaf(-x, x, q));
-}
-__device__ __forceinline__ float normal_cdf(float z) {
-  const float q = normal_tail(z);
-  return z < 0.f ? q : 1.f - q;
+// Of two values at once, in packed arithmetic.
+__device__ __forceinline__ void normal_cdf2(float z0, float z1, float& c0, float& c1) {
+  float x0, x1, t0, t1, q0, q1;
+  mul2(x0, x1, fabsf(z0), fabsf(z1), 0.70710678f, 0.70710678f);
+  fma2(t0, t1, x0, x1, 0.5f, 0.5f, 1.f, 1.f);
+  t0 = __fdividef(1.f, t0);
+  t1 = __fdividef(1.f, t1);
+  fma2(q0, q1, t0, t1, 0.17087277f, 0.17087277f, -0.82215223f, -0.82215223f);
+  fma2(q0, q1, t0, t1, q0, q1, 1.48851587f, 1.48851587f);
+  fma2(q0, q1, t0, t1, q0, q1, -1.13520398f, -1.13520398f);
+  fma2(q0, q1, t0, t1, q0, q1, 0.27886807f, 0.27886807f);
+  fma2(q0, q1, t0, t1, q0, q1, -0.18628806f, -0.18628806f);
+  fma2(q0, q1, t0, t1, q0, q1, 0.09678418f, 0.09678418f);
+  fma2(q0, q1, t0, t1, q0, q1, 0.37409196f, 0.37409196f);
+  fma2(q0, q1, t0, t1, q0, q1, 1.00002368f, 1.00002368f);
+  fma2(q0, q1, t0, t1, q0, q1, -1.26551223f, -1.26551223f);
+  fma2(q0, q1, -x0, -x1, x0, x1, q0, q1);
+  mul2(t0, t1, t0, t1, 0.5f, 0.5f);
+  mul2(q0, q1, t0, t1, __expf(q0), __expf(q1));   // erfc(|z| / sqrt 2) / 2
+  c0 = z0 < 0.f ? q0 : 1.f - q0;
+  c1 = z1 < 0.f ? q1 : 1.f - q1;
 }
 __device__ __forceinline__ float gelu_arg(float z) { return 0.79788456f * z * (1.f + 0.044715f * z * z); }
 
@@ -111,9 +116,20 @@ template <int FN>
 __device__ __forceinline__ float act_fn(float z) {
   if (FN == MOE_FN_RELU) return z < 0.f ? 0.f : z;   // (NaN stays NaN)
   if (FN == MOE_FN_SILU) return __fdividef(z, 1.f + __expf(-z));
-  if (FN == MOE_FN_GELU) return z * normal_cdf(z);
   if (FN == MOE_FN_GELU_TANH) return __fdividef(z, 1.f + __expf(-2.f * gelu_arg(z)));
   return z;
+}
+
+template <int FN>
+__device__ __forceinline__ void act_pair(float& a, float& b) {
+  if (FN == MOE_FN_GELU) {
+    float ca, cb;
+    normal_cdf2(a, b, ca, cb);
+    mul2(a, b, a, b, ca, cb);
+  } else {
+    a = act_fn<FN>(a);
+    b = act_fn<FN>(b);
+  }
 }
 
 __device__ __forceinline__ float clamp_hi(float v, float L) { return v > L ? L : v; }    // NaN passes
@@ -526,7 +542,7 @@ __device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t
     store_rows<64>(p, buf, kPitchSw, out, p.ld_out, n, lim, th, p.out, p.out_end);
   } else {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = act_fn<FN>(v[c]);
+    for (int c = 0; c < 32; c += 2) act_pair<FN>(v[c], v[c + 1]);
     if (p.residual) {
       load_rows<128>(buf, kPitch, p.residual + r0 * p.ld_res + t.i0, p.ld_res, n, lim, th);
       group_sync(bar);
@@ -1332,7 +1348,6 @@ __device__ __forceinline__ float act_grad(float z, float dy) {
     const float s = __fdividef(1.f, 1.f + __expf(-z));
     return dy * s * (1.f + z * (1.f - s));
   }
-  if (FN == MOE_FN_GELU) return dy * fmaf(z * 0.39894228f, __expf(-0.5f * z * z), normal_cdf(z));
   if (FN == MOE_FN_GELU_TANH) {   // s = (1 + tanh v) / 2, (1 - tanh^2 v) / 2 = 2 s (1 - s)
     const float s = __fdividef(1.f, 1.f + __expf(-2.f * gelu_arg(z)));
     return dy * (s + 2.f * z * s * (1.f - s) * 0.79788456f * (1.f + 0.134145f * z * z));
@@ -1361,15 +1376,29 @@ __device__ __forceinline__ bool find_chunk(const ActGradParams& p, int q, int& e
 template <int FN>
 __device__ __forceinline__ void act_grad8(const ActGradParams& p, const float (&z)[8], const float (&u)[8],
                                           const float (&dy)[8], float (&o)[8], float (&ou)[8]) {
+  if constexpr (FN == MOE_FN_GELU) {   // Phi(z) + z phi(z)
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (FN == MOE_FN_SWIGLU) {
-      const float g = clamp_hi(z[k], p.limit), uc = clamp_both(u[k], p.limit);
-      const float s = __fdividef(1.f, 1.f + __expf(-g)), gs = g * s;
-      o[k] = z[k] > p.limit ? 0.f : dy[k] * uc * (s + gs * (1.f - s));
-      ou[k] = fabsf(u[k]) <= p.limit ? dy[k] * gs : 0.f;
-    } else {
-      o[k] = act_grad<FN>(z[k], dy[k]);
+    for (int k = 0; k < 8; k += 2) {
+      float c0, c1, e0, e1;
+      normal_cdf2(z[k], z[k + 1], c0, c1);
+      mul2(e0, e1, z[k], z[k + 1], z[k], z[k + 1]);
+      e0 = __expf(-0.5f * e0);
+      e1 = __expf(-0.5f * e1);
+      mul2(e0, e1, e0, e1, 0.39894228f, 0.39894228f);
+      fma2(c0, c1, z[k], z[k + 1], e0, e1, c0, c1);
+      mul2(o[k], o[k + 1], dy[k], dy[k + 1], c0, c1);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (FN == MOE_FN_SWIGLU) {
+        const float g = clamp_hi(z[k], p.limit), uc = clamp_both(u[k], p.limit);
+        const float s = __fdividef(1.f, 1.f + __expf(-g)), gs = g * s;
+        o[k] = z[k] > p.limit ? 0.f : dy[k] * uc * (s + gs * (1.f - s));
+        ou[k] = fabsf(u[k]) <= p.limit ? dy[k] * gs : 0.f;
+      } else {
+        o[k] = act_grad<FN>(z[k], dy[k]);
+      }
     }
   }
 }
