@@ -1217,6 +1217,26 @@ int launch_split_of(const LinArgs& a) {
   return err == cudaSuccess ? 1 : -1;
 }
 
+// Width of a pair's tiles along j: the one whose turns on `pairs` pairs take least.  A stage of a
+// w-wide tile takes the longer of its MMAs (2 w cycles) and its copies (128 rows of A and w / 2 of
+// B, 2 cycles a row), a turn about 96 cycles a stage more (its epilogue's share).  1024 x 2880 x
+// 5760: 92 tiles of 256 are two turns of 74 pairs (33.6 us), 138 of 192 are two as well (30.6 us).
+// Ragged rows: 256.
+int pair_width(const LinArgs& a, int n_it, int pairs) {
+  if (a.offsets && a.mode != kWeightGrad) return 256;
+  const int64_t J = a.mode == kWeightGrad ? a.N : a.rows, experts = a.mode == kWeightGrad ? a.E : 1;
+  int best = 256;
+  int64_t least = -1;
+  for (int w = 256; w >= 64; w -= 32) {
+    const int64_t tiles = experts * ((J + w - 1) / w) * n_it, cost = (tiles + pairs - 1) / pairs * (std::max(2 * w, 256 + w) + 96);
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = w;
+    }
+  }
+  return best;
+}
+
 // Clusters of two CTAs of `kern` that the device holds at once, remembered per device.
 template <class K>
 int pair_slots(K kern, int threads, int smem, std::atomic<int>* known) {
@@ -1251,8 +1271,6 @@ int launch_pair_of(const LinArgs& a) {
   for (uint32_t m = 0; m < (MODE == kWeightGrad ? 1 : 4); ++m)
     if (!b_map(a, 32 * (m + 1), &mb.m[m])) return -1;
   LinParams p = params_of(a, SW ? 128 : 256);
-  p.nw_max = C::NB;
-  p.n_jt = (a.N + C::NB - 1) / C::NB;
   p.splits = 1;
   auto kern = lin_pair_kernel<MODE, SW, BF>;
   static std::atomic<uint64_t> done{0};
@@ -1260,7 +1278,9 @@ int launch_pair_of(const LinArgs& a) {
   if (!allow_smem(kern, C::SMEM, done)) return -1;
   const int n = pair_slots(kern, C::THREADS, C::SMEM, slots);
   if (n <= 0) return -1;
-  const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, C::NB)) * p.n_it;
+  p.nw_max = pair_width(a, p.n_it, n);
+  p.n_jt = (a.N + p.nw_max - 1) / p.nw_max;
+  const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, p.nw_max)) * p.n_it;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, n);
   return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, false, 2u, ma, mb, p) ==
                  cudaSuccess ? 1 : -1;
