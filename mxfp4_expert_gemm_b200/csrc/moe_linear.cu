@@ -334,14 +334,19 @@ __device__ __forceinline__ void build_table(const LinParams& p, RowTable* tab, i
 }
 
 // The item-th tile (< items) of `units` pairs taking tiles in turn, by the whole warp.  Tiles are
-// listed expert by expert, dearest first, along i fastest; the turns come from both ends of that
-// list, each pair changing ends every time: large experts' tiles, bound by the tensor cores, then
-// run beside small experts', bound by the bytes of their weights (or of dW).
+// listed expert by expert, dearest first, and within an expert along the axis with fewer tiles
+// fastest: the tiles that run side by side then share the operand that is read once, and the
+// other, smaller one stays in L2 (along i always: 4096 rows x 8 experts read 455 MB for 289 MB of
+// operands, the weights again for each token tile; 301 MB so).  A weight gradient, bound by its
+// writes, goes along i, so that whole rows of dW are written at one time (490 us, 520 along j).
+// The turns come from both ends of the list, each pair changing ends every time: large experts'
+// tiles, bound by the tensor cores, then run beside small experts', bound by the bytes of their
+// weights.  (A weight gradient's tiles all write as much: in order, 2-4% faster.)
 template <int MODE>
 __device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable* tab, uint32_t item, uint32_t units,
                                               int step, int iw) {
   const int lane = threadIdx.x & 31;
-  if (p.E > 1) {
+  if (MODE != kWeightGrad && p.E > 1) {
     const uint32_t r = item / units, u = item - r * units;
     const uint32_t k = units & 1 ? item >> 1 : r * (units >> 1) + (u >> 1);   // turns of that end so far
     item = ((r + u) & 1) == 0 ? k : tab->items - 1 - k;
@@ -349,7 +354,6 @@ __device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable
   const int q = item / (uint32_t)p.n_it;
   LinTile t;
   t.ok = 1;
-  t.i0 = (int)(item - (uint32_t)q * p.n_it) * iw;
   int rank = 0;
   if (p.E > 1) {   // the lane, then the rank of its eight, whose tiles hold q
     const unsigned m = __ballot_sync(0xffffffffu, tab->base[8 * lane] <= q && q < tab->base[8 * lane + 8]);
@@ -358,7 +362,15 @@ __device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable
     rank = 8 * (__ffs(m) - 1) + __ffs(m8) - 1;
   }
   t.e = p.E > 1 ? tab->order[rank] : 0;
-  const int jt = q - tab->base[rank], cnt = tab->cnt[t.e], start = tab->start[t.e];
+  const int first = tab->base[rank], nt = tab->base[rank + 1] - first;
+  const int cnt = tab->cnt[t.e], start = tab->start[t.e];
+  int jt = q - first, it = item - (uint32_t)q * p.n_it;
+  if (MODE != kWeightGrad && nt <= p.n_it) {
+    const uint32_t loc = item - (uint32_t)first * p.n_it;
+    it = loc / (uint32_t)nt;
+    jt = loc - (uint32_t)it * nt;
+  }
+  t.i0 = it * iw;
   if (MODE == kWeightGrad) {
     const int w = tile_width(p.J, p.n_jt, step);
     t.j0 = jt * w;
