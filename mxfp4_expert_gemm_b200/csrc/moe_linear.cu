@@ -333,24 +333,15 @@ __device__ __forceinline__ void build_table(const LinParams& p, RowTable* tab, i
   }
 }
 
-// The item-th tile (< items) of `units` pairs taking tiles in turn, by the whole warp.  Tiles are
-// listed expert by expert, dearest first, and within an expert along the axis with fewer tiles
-// fastest: the tiles that run side by side then share the operand that is read once, and the
-// other, smaller one stays in L2 (along i always: 4096 rows x 8 experts read 455 MB for 289 MB of
-// operands, the weights again for each token tile; 301 MB so).  A weight gradient, bound by its
-// writes, goes along i, so that whole rows of dW are written at one time (490 us, 520 along j).
-// The turns come from both ends of the list, each pair changing ends every time: large experts'
-// tiles, bound by the tensor cores, then run beside small experts', bound by the bytes of their
-// weights.  (A weight gradient's tiles all write as much: in order, 2-4% faster.)
+// Tile `item` (< items) by the whole warp.  Tiles are listed expert by expert, dearest first, and
+// within an expert along the axis with fewer tiles fastest: the tiles that run side by side then
+// share the operand that is read once, and the other, smaller one stays in L2 (along i always:
+// 4096 rows x 8 experts read 455 MB for 289 MB of operands, the weights again for each token tile;
+// 301 MB so).  A weight gradient, bound by its writes, goes along i, so that whole rows of dW are
+// written at one time (490 us, 520 along j).
 template <int MODE>
-__device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable* tab, uint32_t item, uint32_t units,
-                                              int step, int iw) {
+__device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable* tab, uint32_t item, int step, int iw) {
   const int lane = threadIdx.x & 31;
-  if (MODE != kWeightGrad && p.E > 1) {
-    const uint32_t r = item / units, u = item - r * units;
-    const uint32_t k = units & 1 ? item >> 1 : r * (units >> 1) + (u >> 1);   // turns of that end so far
-    item = ((r + u) & 1) == 0 ? k : tab->items - 1 - k;
-  }
   const int q = item / (uint32_t)p.n_it;
   LinTile t;
   t.ok = 1;
@@ -952,7 +943,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     int g = 0;
     bool stop = false, withheld = false;
     for (uint32_t item = unit0; item < n_items && !stop; item += units) {
-      const LinTile t = table_tile<MODE>(p, tab, item, units, C::STEP, kIW);
+      const LinTile t = table_tile<MODE>(p, tab, item, C::STEP, kIW);
       const int kb_all = (t.clen + kBK - 1) / kBK, half = t.nw / 2;
       const int boxes = (half + 31) / 32;   // B's rows in units of 32, as one copy
       const bool narrow = half <= 64;       // (kWeightGrad: one or two 64-wide copies)
@@ -1017,7 +1008,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       int li = 0;
       bool stop = false;
       for (uint32_t item = unit0; item < n_items && !stop; item += units, ++li) {
-        const LinTile t = table_tile<MODE>(p, tab, item, units, C::STEP, kIW);
+        const LinTile t = table_tile<MODE>(p, tab, item, C::STEP, kIW);
         const int kb_all = (t.clen + kBK - 1) / kBK, b2 = li & 1;
         const uint32_t idesc = ptx::idesc_f16(BF, 256, t.nw, C::A_MN, C::B_MN);
         if (li >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait_cluster_bounded(
@@ -1059,7 +1050,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     const int q = warp & 3, row = 32 * q + lane, part = (warp - 2) >> 2;
     int li = 0;
     for (uint32_t item = unit0; item < n_items; item += units, ++li) {
-      LinTile t = table_tile<MODE>(p, tab, item, units, C::STEP, kIW);
+      LinTile t = table_tile<MODE>(p, tab, item, C::STEP, kIW);
       t.i0 += kIW / 2 * rank;
       const int b2 = li & 1;
       const bool have = t.clen > 0;
