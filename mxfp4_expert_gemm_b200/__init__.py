@@ -1,7 +1,7 @@
 """Python binding of ``libmoe_mxfp4.so``: the B200 MoE layer with MXFP4 experts.
 
-Argument marshalling only: every step of the layer runs in the library's CUDA
-kernels.  PyTorch provides device memory and the current stream.  The C ABI and
+Argument marshalling only (the short calls' in binding/marshal.cpp): every step of the layer runs
+in the library's CUDA kernels.  PyTorch provides device memory and the current stream.  The C ABI and
 its contract are in ``include/moe_mxfp4.h``; the functions here carry the same
 names.  There is no fallback: if the library is missing or the device is not
 sm_100, the calls raise.
@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
-import functools
+import importlib.util
 import os
 import re
 import threading
@@ -77,6 +77,7 @@ def make_dims(d: int, I: int, E: int, top_k: int, rms_eps: float = 1e-5, swiglu_
 
 
 _lib = None
+_marshal = None   # the compiled part of the binding, bound to _lib
 _lock = threading.Lock()
 
 
@@ -88,7 +89,29 @@ def lib():
             if not os.path.exists(LIB_PATH):
                 raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m mxfp4_expert_gemm_b200.build`")
             _lib = load_library(LIB_PATH)
+            _bind(_lib)
     return _lib
+
+
+def _bind(L) -> None:
+    """Point the compiled argument marshalling at a build of the library."""
+    global _marshal
+    if _marshal is None:
+        path = os.path.join(_PKG, "_marshal.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m mxfp4_expert_gemm_b200.build`")
+        spec = importlib.util.spec_from_file_location("_marshal", path)
+        _marshal = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_marshal)
+    _marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        L.moe_norm, L.moe_norm_backward, L.moe_norm_workspace_bytes, L.moe_linear, L.moe_linear_backward,
+        L.moe_grouped_linear, L.moe_grouped_linear_backward, L.moe_linear_workspace_bytes)))
+
+
+def _calls():
+    if _lib is None:
+        lib()
+    return _marshal
 
 
 @contextlib.contextmanager
@@ -100,11 +123,13 @@ def use_library(path: str):
     prev = lib()
     with _lock:
         _lib = other
+        _bind(other)
     try:
         yield other
     finally:
         with _lock:
             _lib = prev
+            _bind(prev)
 
 
 def load_library(path: str):
@@ -482,120 +507,33 @@ def moe_debug_inject_timeout(enable: bool = True) -> None:
 
 
 # ----------------------------------------------------------- norms and 16-bit products, with gradients
-# These calls are short enough on the GPU (2-10 us) for the host's part to show, so their checks
-# read a tensor's properties once and the stream as a plain handle.
-try:
-    from torch._C import _cuda_getCurrentRawStream as _current_raw_stream
-except ImportError:
-    def _current_raw_stream(device: int) -> int:
-        return torch.cuda.current_stream(device).cuda_stream
+# Checks, allocations and the calls themselves are in binding/marshal.cpp.
+def _handle(stream):
+    return None if stream is None else stream.cuda_stream
 
 
-def _here(t, name) -> int:
-    """The device index of a call's first tensor, which has to be the current one."""
-    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
-    if dev < 0:
-        raise TypeError(f"{name}: a CUDA tensor is required")
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"{name}: on cuda:{dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    return dev
+def _named(name, table, what) -> int:
+    i = table.get(name)
+    if i is None:
+        raise ValueError(f"{what}: {name!r}, expected one of {sorted(table)}")
+    return i
 
 
-def _rows(t, dtype, name, dev, rows, cols) -> int:
-    """Row stride of a [rows, cols] tensor whose columns are contiguous."""
-    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
-        raise TypeError(f"{name}: a CUDA tensor is required")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
-    if t.shape != (rows, cols):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
-    ld, one = t.stride()
-    if one != 1 and cols != 1:
-        raise ValueError(f"{name}: the columns of a row must be contiguous")
-    return cols if rows <= 1 and ld < cols else ld
-
-
-def _flat(t, dtype, name, dev, shape):
-    """The address of a contiguous tensor of the given shape (None for None)."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor) or t.get_device() < 0:
-        raise TypeError(f"{name}: a CUDA tensor is required")
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
-
-
-def _raw_stream(stream, dev) -> int:
-    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
-
-
-def _status(status_word, dev):
-    return None if status_word is None else _flat(status_word, torch.int32, "status_word", dev, status_word.shape)
-
-
-def _workspace(ws, nbytes, like, dev, stream):
-    """(tensor, address, bytes) of a caller's workspace, or of one taken from torch's allocator (which
-    must not hand it on before a `stream` other than the current one has passed the call)."""
-    if ws is None:
-        ws = like.new_empty((nbytes + like.element_size() - 1) // like.element_size())
-        if stream is not None:
-            ws.record_stream(stream)
-    elif not isinstance(ws, torch.Tensor) or ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError(f"ws: a contiguous tensor on cuda:{dev} is required")
-    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
-
-
-def _rows_like(x, rows, cols):
-    """An output of x's type; torch's cheapest allocation where x's shape and strides are its own."""
-    return torch.empty_like(x) if x.is_contiguous() and x.shape[1] == cols else x.new_empty((rows, cols))
-
-
-@functools.lru_cache(maxsize=256)
-def _norm_scratch(T: int, d: int) -> int:
-    return lib().moe_norm_workspace_bytes(T, d)
-
-
-def _norm_args(x, kind):
-    dev = _here(x, "x")
-    dt = DTYPES.get(x.dtype)
-    if dt is None:
-        raise TypeError(f"x: dtype {x.dtype}")
-    k = NORM_KINDS.get(kind)
-    if k is None:
-        raise ValueError(f"kind: {kind!r}, expected one of {sorted(NORM_KINDS)}")
-    if x.dim() != 2:
-        raise ValueError(f"x: shape {tuple(x.shape)}, expected [rows, columns]")
-    T, d = x.shape
-    return dev, dt, k, T, d, _rows(x, x.dtype, "x", dev, T, d)
+def _scratch_on(stream, nbytes: int, like):
+    """Scratch for a call on a stream that is not the current one: torch's allocator must not hand it
+    on before that stream has passed the call."""
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
+    ws.record_stream(stream)
+    return ws
 
 
 def moe_norm(x, w, b=None, kind="rms", eps=1e-5, y=None, want_stats=False, stream=None):
     """y [T, d] = RMSNorm(x) * w (kind "rms") or LayerNorm(x) * w + b (kind "layer"); bf16, fp16
     or fp32 rows, fp32 w and b.  With want_stats: (y, mean, rstd) for moe_norm_backward (mean is
     None for "rms")."""
-    dev, dt, k, T, d, ldx = _norm_args(x, kind)
-    wp = _flat(w, torch.float32, "w", dev, (d,))
-    if y is None:
-        y, ldy = _rows_like(x, T, d), d
-    else:
-        ldy = _rows(y, x.dtype, "y", dev, T, d)
-    mean = rstd = None
-    if want_stats:
-        rstd = w.new_empty(T)
-        mean = torch.empty_like(rstd) if k == 1 else None
-    _check((_lib or lib()).moe_norm(k, dt, T, d, x.data_ptr(), ldx, wp,
-                                    _flat(b, torch.float32, "b", dev, (d,)), eps, y.data_ptr(), ldy,
-                                    None if mean is None else mean.data_ptr(),
-                                    None if rstd is None else rstd.data_ptr(), _raw_stream(stream, dev)), "moe_norm")
+    st, y, mean, rstd = _calls().norm(x, w, b, _named(kind, NORM_KINDS, "kind"), eps, y, want_stats, _handle(stream))
+    if st:
+        raise MoeError(st, "moe_norm")
     return (y, mean, rstd) if want_stats else y
 
 
@@ -608,125 +546,46 @@ def moe_norm_backward(dy, x, w, mean, rstd, kind="rms", dres=None, dx=None, need
     """(dx, dw, db) of moe_norm, with dres (a gradient of dx's shape) added to dx in the same pass.
     dw and db are fp32 [d]; db ("layer" only) defaults to kind == "layer" and is None when not
     asked for."""
-    dev, dt, k, T, d, ldx = _norm_args(x, kind)
+    k = _named(kind, NORM_KINDS, "kind")
     if need_db is None:
         need_db = k == 1
-    lddy = _rows(dy, x.dtype, "dy", dev, T, d)
-    lddres = 0 if dres is None else _rows(dres, x.dtype, "dres", dev, T, d)
-    wp = _flat(w, torch.float32, "w", dev, (d,))
-    if dx is None:
-        dx, lddx = _rows_like(x, T, d), d
-    else:
-        lddx = _rows(dx, x.dtype, "dx", dev, T, d)
-    dw = torch.empty_like(w) if need_dw else None
-    db = torch.empty_like(w) if need_db else None
-    ws_ptr, ws_bytes = None, 0
-    if need_dw or need_db:
-        ws, ws_ptr, ws_bytes = _workspace(ws, _norm_scratch(T, d), x, dev, stream)
-    _check((_lib or lib()).moe_norm_backward(
-        k, dt, T, d, dy.data_ptr(), lddy, x.data_ptr(), ldx, wp,
-        _flat(mean, torch.float32, "mean", dev, (T,)), _flat(rstd, torch.float32, "rstd", dev, (T,)),
-        None if dres is None else dres.data_ptr(), lddres, dx.data_ptr(), lddx,
-        None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(), ws_ptr, ws_bytes,
-        _raw_stream(stream, dev)), "moe_norm_backward")
+    if stream is not None and ws is None and x.dim() == 2:
+        ws = _scratch_on(stream, moe_norm_workspace_bytes(*x.shape), x)
+    st, dx, dw, db = _calls().norm_backward(dy, x, w, mean, rstd, k, dres, dx, need_dw, need_db, ws, _handle(stream))
+    if st:
+        raise MoeError(st, "moe_norm_backward")
     return dx, dw, db
 
 
-@functools.lru_cache(maxsize=256)
 def make_linear_dims(K: int, N: int, E: int = 1, dtype=torch.bfloat16, fn: str = "none",
                      limit: float = 7.0) -> moe_linear_dims:
-    if fn not in FNS:
-        raise ValueError(f"fn: {fn!r}, expected one of {sorted(FNS)}")
     if dtype not in (torch.bfloat16, torch.float16):
         raise TypeError(f"the products take bf16 or fp16 tensors, not {dtype}")
-    return moe_linear_dims(K, N, E, DTYPES[dtype], FNS[fn], limit)
+    return moe_linear_dims(K, N, E, DTYPES[dtype], _named(fn, FNS, "fn"), limit)
 
 
 def moe_linear_workspace_bytes(dims: moe_linear_dims, rows: int) -> int:
     return lib().moe_linear_workspace_bytes(ctypes.byref(dims), rows)
 
 
-@functools.lru_cache(maxsize=256)
-def _linear_scratch(K, N, E, dtype, fn, limit, rows):
-    return moe_linear_workspace_bytes(make_linear_dims(K, N, E, dtype, fn, limit), rows)
-
-
-def _product_dims(x, w, grouped, fn, limit):
-    """(device, rows, row stride of x, dims) of a product's x [rows, K] and w [N, K] ([E, N, K])."""
-    dev = _here(x, "x")
-    if x.dim() != 2 or not isinstance(w, torch.Tensor) or w.dim() != (3 if grouped else 2) or w.shape[-1] != x.shape[1]:
-        raise ValueError(f"x [rows, K] and w {'[E, N, K]' if grouped else '[N, K]'} are required")
-    rows, K = x.shape
-    ldx = _rows(x, x.dtype, "x", dev, rows, K)
-    _flat(w, x.dtype, "w", dev, w.shape)
-    return dev, rows, ldx, make_linear_dims(K, w.shape[-2], w.shape[0] if grouped else 1, x.dtype, fn, limit)
-
-
 def _forward_product(what, x, w, offsets, bias, fn, limit, residual, y, z, want_z, status_word, stream):
-    grouped = offsets is not None
-    dev, rows, ldx, dims = _product_dims(x, w, grouped, fn, limit)
-    N = dims.N
-    No = N // 2 if fn == "swiglu" else N
-    if y is None:
-        y, ldy = x.new_empty((rows, No)), No
-    else:
-        ldy = _rows(y, x.dtype, "y", dev, rows, No)
-    if want_z and z is None:
-        z = x.new_empty((rows, N))
-    zp = _flat(z, x.dtype, "z", dev, (rows, N))
-    bp = _flat(bias, torch.float32, "bias", dev, (dims.E, N) if grouped else (N,))
-    sp = _status(status_word, dev)
-    L = _lib or lib()
-    if grouped:
-        op = _flat(offsets, torch.int32, "offsets", dev, (dims.E + 1,))
-        st = L.moe_grouped_linear(ctypes.byref(dims), rows, x.data_ptr(), ldx, w.data_ptr(), op, bp, y.data_ptr(), ldy,
-                                  zp, sp, _raw_stream(stream, dev))
-    else:
-        rp, ldr = None, 0
-        if residual is not None:
-            rp, ldr = residual.data_ptr(), _rows(residual, x.dtype, "residual", dev, rows, No)
-        st = L.moe_linear(ctypes.byref(dims), rows, x.data_ptr(), ldx, w.data_ptr(), bp, rp, ldr, y.data_ptr(), ldy, zp,
-                          sp, _raw_stream(stream, dev))
-    _check(st, what)
+    st, y, z = _calls().product(x, w, offsets, bias, _named(fn, FNS, "fn"), limit, residual, y, z, want_z, status_word,
+                                _handle(stream))
+    if st:
+        raise MoeError(st, what)
     return (y, z) if want_z else y
 
 
 def _backward_product(what, dy, x, w, offsets, z, fn, limit, dx, dw, need_dx, need_dw, need_db, ws, status_word,
                       stream):
-    grouped = offsets is not None
-    dev, rows, ldx, dims = _product_dims(x, w, grouped, fn, limit)
-    K, N = dims.K, dims.N
-    lddy = _rows(dy, x.dtype, "dy", dev, rows, N // 2 if fn == "swiglu" else N)
-    if fn != "none" and z is None:
-        raise ValueError(f"z: the forward pass's pre-activation is required with fn={fn!r}")
-    zp = _flat(z, x.dtype, "z", dev, (rows, N)) if fn != "none" else None
-    dxp, lddx, dwp, db, dbp = None, 0, None, None, None
-    if dx is not None:
-        dxp, lddx = dx.data_ptr(), _rows(dx, x.dtype, "dx", dev, rows, K)
-    elif need_dx:
-        dx, lddx = _rows_like(x, rows, K), K
-        dxp = dx.data_ptr()
-    if dw is not None:
-        dwp = _flat(dw, x.dtype, "dw", dev, w.shape)
-    elif need_dw:
-        dw = torch.empty_like(w)
-        dwp = dw.data_ptr()
-    if need_db:
-        db = torch.empty(w.shape[:-1], dtype=torch.float32, device=x.device)
-        dbp = db.data_ptr()
-    ws_ptr, ws_bytes = None, 0
-    if fn != "none" or need_db:
-        ws, ws_ptr, ws_bytes = _workspace(ws, _linear_scratch(K, N, dims.E, x.dtype, fn, limit, rows), x, dev, stream)
-    common = (zp, dxp, lddx, dwp, dbp, ws_ptr, ws_bytes, _status(status_word, dev), _raw_stream(stream, dev))
-    L = _lib or lib()
-    if grouped:
-        op = _flat(offsets, torch.int32, "offsets", dev, (dims.E + 1,))
-        st = L.moe_grouped_linear_backward(ctypes.byref(dims), rows, dy.data_ptr(), lddy, x.data_ptr(), ldx,
-                                           w.data_ptr(), op, *common)
-    else:
-        st = L.moe_linear_backward(ctypes.byref(dims), rows, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(),
-                                   *common)
-    _check(st, what)
+    f = _named(fn, FNS, "fn")
+    if stream is not None and ws is None and x.dim() == 2 and w.dim() in (2, 3):
+        dims = make_linear_dims(x.shape[1], w.shape[-2], w.shape[0] if w.dim() == 3 else 1, x.dtype, fn, limit)
+        ws = _scratch_on(stream, moe_linear_workspace_bytes(dims, x.shape[0]), x)
+    st, dx, dw, db = _calls().product_backward(dy, x, w, offsets, z, f, limit, dx, dw, need_dx, need_dw, need_db, ws,
+                                               status_word, _handle(stream))
+    if st:
+        raise MoeError(st, what)
     return dx, dw, db
 
 

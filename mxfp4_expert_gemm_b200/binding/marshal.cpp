@@ -1,0 +1,385 @@
+// Tensor arguments of the norms and 16-bit products, checked and handed to the C library.
+//
+// These calls take 2-10 us on the GPU at serving sizes; in Python their checks and allocations took
+// as long again (a product 11.5 us a call, 4.7 of them in the library).  The rest of the binding
+// stays in Python.  Functions take positional arguments from the wrappers in __init__.py and return
+// (status, outputs ...).
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <cstdint>
+#include <string>
+
+#include "moe_mxfp4.h"
+
+namespace {
+
+// Addresses in the library that is in use (set by bind()).
+struct Calls {
+  decltype(&moe_norm) norm = nullptr;
+  decltype(&moe_norm_backward) norm_backward = nullptr;
+  decltype(&moe_norm_workspace_bytes) norm_workspace = nullptr;
+  decltype(&moe_linear) linear = nullptr;
+  decltype(&moe_linear_backward) linear_backward = nullptr;
+  decltype(&moe_grouped_linear) grouped = nullptr;
+  decltype(&moe_grouped_linear_backward) grouped_backward = nullptr;
+  decltype(&moe_linear_workspace_bytes) workspace = nullptr;
+} g_calls;
+
+struct Bad {   // an argument error: a Python exception of this type
+  PyObject* type;
+  std::string text;
+};
+
+std::string str(const char* s) { return s; }
+
+std::string shape_of(const at::Tensor& t) {
+  std::string s = "(";
+  for (int64_t i = 0; i < t.dim(); ++i) s += (i ? ", " : "") + std::to_string(t.size(i));
+  return s + ")";
+}
+
+const at::Tensor& cuda_tensor(PyObject* o, const char* name) {
+  if (!THPVariable_Check(o)) throw Bad{PyExc_TypeError, str(name) + ": a CUDA tensor is required"};
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_cuda()) throw Bad{PyExc_TypeError, str(name) + ": a CUDA tensor is required"};
+  return t;
+}
+
+const at::Tensor& checked(PyObject* o, const char* name, at::ScalarType type, int dev) {
+  const at::Tensor& t = cuda_tensor(o, name);
+  if (t.scalar_type() != type)
+    throw Bad{PyExc_TypeError, str(name) + ": dtype " + c10::toString(t.scalar_type()) + ", expected " + c10::toString(type)};
+  if (t.get_device() != dev)
+    throw Bad{PyExc_ValueError, str(name) + ": on cuda:" + std::to_string(t.get_device()) + ", expected cuda:" + std::to_string(dev)};
+  return t;
+}
+
+// The call's first tensor [rows, cols]; its device has to be the current one.
+const at::Tensor& first_tensor(PyObject* o, const char* name) {
+  const at::Tensor& t = cuda_tensor(o, name);
+  const int now = c10::cuda::current_device();
+  if (t.get_device() != now)
+    throw Bad{PyExc_ValueError, str(name) + ": on cuda:" + std::to_string(t.get_device()) + ", but the current device is cuda:" +
+                                    std::to_string(now)};
+  if (t.dim() != 2 || t.size(0) > INT32_MAX || t.size(1) > INT32_MAX)
+    throw Bad{PyExc_ValueError, str(name) + ": shape " + shape_of(t) + ", expected [rows, columns]"};
+  return t;
+}
+
+// Row stride of a [rows, cols] tensor whose columns are contiguous.
+int64_t row_stride(const at::Tensor& t, const char* name, int64_t rows, int64_t cols) {
+  if (t.dim() != 2 || t.size(0) != rows || t.size(1) != cols)
+    throw Bad{PyExc_ValueError, str(name) + ": shape " + shape_of(t) + ", expected (" + std::to_string(rows) + ", " + std::to_string(cols) + ")"};
+  if (t.stride(1) != 1 && cols != 1) throw Bad{PyExc_ValueError, str(name) + ": the columns of a row must be contiguous"};
+  const int64_t ld = t.stride(0);
+  return rows <= 1 && ld < cols ? cols : ld;
+}
+
+// Address of a contiguous tensor of the given shape (NULL for None).
+void* flat(PyObject* o, const char* name, at::ScalarType type, int dev, at::IntArrayRef shape) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = checked(o, name, type, dev);
+  if (t.sizes() != shape) throw Bad{PyExc_ValueError, str(name) + ": shape " + shape_of(t) + " is not the expected one"};
+  if (!t.is_contiguous()) throw Bad{PyExc_ValueError, str(name) + ": must be contiguous"};
+  return t.data_ptr();
+}
+
+struct Rows {   // a [rows, cols] operand: given, or (where `make`) made here
+  at::Tensor t;
+  void* p = nullptr;
+  int64_t ld = 0;
+};
+Rows rows_arg(PyObject* o, const char* name, at::ScalarType type, int dev, int64_t rows, int64_t cols) {
+  Rows r;
+  if (o == Py_None) return r;
+  r.t = checked(o, name, type, dev);
+  r.ld = row_stride(r.t, name, rows, cols);
+  r.p = r.t.data_ptr();
+  return r;
+}
+Rows rows_out(PyObject* o, const char* name, const at::Tensor& like, int dev, int64_t rows, int64_t cols, bool make) {
+  Rows r = rows_arg(o, name, like.scalar_type(), dev, rows, cols);
+  if (o == Py_None && make) {
+    r.t = at::empty({rows, cols}, like.options());
+    r.p = r.t.data_ptr();
+    r.ld = cols;
+  }
+  return r;
+}
+
+void* raw_stream(PyObject* o, int dev) {
+  if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+  void* s = PyLong_AsVoidPtr(o);
+  if (PyErr_Occurred()) throw python_error();
+  return s;
+}
+
+struct Scratch {
+  at::Tensor t;
+  void* p = nullptr;
+  size_t n = 0;
+};
+Scratch scratch(PyObject* o, size_t bytes, const at::Tensor& like, int dev) {
+  Scratch s;
+  if (o == Py_None) {
+    s.t = at::empty({(int64_t)((bytes + 3) / 4)}, like.options().dtype(at::kFloat));
+  } else {
+    s.t = cuda_tensor(o, "ws");
+    if (s.t.get_device() != dev || !s.t.is_contiguous())
+      throw Bad{PyExc_ValueError, "ws: a contiguous tensor on cuda:" + std::to_string(dev) + " is required"};
+  }
+  s.p = s.t.data_ptr();
+  s.n = s.t.nbytes();
+  return s;
+}
+
+int32_t status_of(PyObject* o, int dev, void** p) {
+  *p = nullptr;
+  if (o != Py_None) {
+    const at::Tensor& t = checked(o, "status_word", at::kInt, dev);
+    if (!t.is_contiguous()) throw Bad{PyExc_ValueError, "status_word: must be contiguous"};
+    *p = t.data_ptr();
+  }
+  return 0;
+}
+
+int dtype_of(const at::Tensor& x, bool fp32) {
+  switch (x.scalar_type()) {
+    case at::kBFloat16: return MOE_DTYPE_BF16;
+    case at::kHalf: return MOE_DTYPE_F16;
+    case at::kFloat:
+      if (fp32) return MOE_DTYPE_F32;
+    default: throw Bad{PyExc_TypeError, str("x: dtype ") + c10::toString(x.scalar_type()) + (fp32 ? "" : ": the products take bf16 or fp16 tensors")};
+  }
+}
+
+PyObject* wrap(const at::Tensor& t) {
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(t);
+}
+// (status, outputs): an output that was given is returned as it came.
+PyObject* result(int status, std::initializer_list<std::pair<PyObject*, const at::Tensor*>> outs) {
+  PyObject* r = PyTuple_New(1 + (Py_ssize_t)outs.size());
+  if (!r) return nullptr;
+  PyTuple_SET_ITEM(r, 0, PyLong_FromLong(status));
+  Py_ssize_t i = 1;
+  for (auto& o : outs) {
+    PyObject* v;
+    if (o.first && o.first != Py_None) v = Py_NewRef(o.first);
+    else v = wrap(*o.second);
+    PyTuple_SET_ITEM(r, i++, v);
+  }
+  return r;
+}
+
+bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+
+double number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (PyErr_Occurred()) throw python_error();
+  return v;
+}
+int64_t whole(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (PyErr_Occurred()) throw python_error();
+  return v;
+}
+
+#define BEGIN(count)                                                       \
+  HANDLE_TH_ERRORS                                                         \
+  if (n != count) {                                                        \
+    PyErr_SetString(PyExc_TypeError, "wrong number of arguments");         \
+    return nullptr;                                                        \
+  }                                                                        \
+  try {
+#define END                                                                \
+  } catch (const Bad& b) {                                                 \
+    PyErr_SetString(b.type, b.text.c_str());                               \
+    return nullptr;                                                        \
+  }                                                                        \
+  END_HANDLE_TH_ERRORS
+
+// x, w, b, kind, eps, y, want_stats, stream -> (status, y, mean, rstd)
+PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BEGIN(8)
+  const at::Tensor& x = first_tensor(a[0], "x");
+  const int dev = x.get_device(), dt = dtype_of(x, true), kind = (int)whole(a[3]);
+  const int64_t T = x.size(0), d = x.size(1), ldx = row_stride(x, "x", T, d);
+  void* w = flat(a[1], "w", at::kFloat, dev, {d});
+  void* b = flat(a[2], "b", at::kFloat, dev, {d});
+  const Rows y = rows_out(a[5], "y", x, dev, T, d, true);
+  at::Tensor mean, rstd;
+  if (truth(a[6])) {
+    const auto o = x.options().dtype(at::kFloat);
+    rstd = at::empty({T}, o);
+    if (kind == MOE_NORM_LAYER) mean = at::empty({T}, o);
+  }
+  const int st = g_calls.norm(kind, dt, (int32_t)T, (int32_t)d, x.data_ptr(), ldx, static_cast<float*>(w),
+                              static_cast<float*>(b), (float)number(a[4]), y.p, y.ld,
+                              mean.defined() ? mean.data_ptr<float>() : nullptr,
+                              rstd.defined() ? rstd.data_ptr<float>() : nullptr, raw_stream(a[7], dev));
+  return result(st, {{a[5], &y.t}, {nullptr, &mean}, {nullptr, &rstd}});
+  END
+}
+
+// dy, x, w, mean, rstd, kind, dres, dx, need_dw, need_db, ws, stream -> (status, dx, dw, db)
+PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BEGIN(12)
+  const at::Tensor& x = first_tensor(a[1], "x");
+  const auto type = x.scalar_type();
+  const int dev = x.get_device(), dt = dtype_of(x, true), kind = (int)whole(a[5]);
+  const int64_t T = x.size(0), d = x.size(1), ldx = row_stride(x, "x", T, d);
+  if (a[0] == Py_None) throw Bad{PyExc_TypeError, "dy: a CUDA tensor is required"};
+  const Rows dy = rows_arg(a[0], "dy", type, dev, T, d), dres = rows_arg(a[6], "dres", type, dev, T, d);
+  void* w = flat(a[2], "w", at::kFloat, dev, {d});
+  void* mean = flat(a[3], "mean", at::kFloat, dev, {T});
+  void* rstd = flat(a[4], "rstd", at::kFloat, dev, {T});
+  const Rows dx = rows_out(a[7], "dx", x, dev, T, d, true);
+  const auto f32 = x.options().dtype(at::kFloat);
+  at::Tensor dw, db;
+  if (truth(a[8])) dw = at::empty({d}, f32);
+  if (truth(a[9])) db = at::empty({d}, f32);
+  Scratch ws;
+  if (dw.defined() || db.defined()) ws = scratch(a[10], g_calls.norm_workspace((int32_t)T, (int32_t)d), x, dev);
+  const int st = g_calls.norm_backward(kind, dt, (int32_t)T, (int32_t)d, dy.p, dy.ld, x.data_ptr(), ldx,
+                                       static_cast<float*>(w), static_cast<float*>(mean), static_cast<float*>(rstd),
+                                       dres.p, dres.ld, dx.p, dx.ld, dw.defined() ? dw.data_ptr<float>() : nullptr,
+                                       db.defined() ? db.data_ptr<float>() : nullptr, ws.p, ws.n, raw_stream(a[11], dev));
+  return result(st, {{a[7], &dx.t}, {nullptr, &dw}, {nullptr, &db}});
+  END
+}
+
+// The operands that both directions of a product have: x [rows, K], w [N, K] ([E, N, K] with offsets).
+struct Product {
+  const at::Tensor& x;
+  const at::Tensor& w;
+  int dev;
+  int64_t rows, ldx, N, No;
+  bool grouped;
+  moe_linear_dims dims;
+};
+Product product_of(PyObject* xo, PyObject* wo, bool grouped, int fn, double limit) {
+  const at::Tensor& x = first_tensor(xo, "x");
+  const int dev = x.get_device(), dt = dtype_of(x, false);
+  const at::Tensor& w = checked(wo, "w", x.scalar_type(), dev);
+  const int64_t rows = x.size(0), K = x.size(1), ldx = row_stride(x, "x", rows, K);
+  if (w.dim() != (grouped ? 3 : 2) || w.size(-1) != K)
+    throw Bad{PyExc_ValueError, str("x [rows, K] and w ") + (grouped ? "[E, N, K]" : "[N, K]") + " are required"};
+  if (!w.is_contiguous()) throw Bad{PyExc_ValueError, "w: must be contiguous"};
+  const int64_t N = w.size(-2), E = grouped ? w.size(0) : 1, most = INT32_MAX;
+  if (rows > most || K > most || N > most || E > most) throw Bad{PyExc_ValueError, "a dimension is beyond 2^31"};
+  return Product{x, w, dev, rows, ldx, N, fn == MOE_FN_SWIGLU ? N / 2 : N, grouped,
+                 moe_linear_dims{(int32_t)K, (int32_t)N, (int32_t)E, dt, fn, (float)limit}};
+}
+
+// x, w, offsets, bias, fn, limit, residual, y, z, want_z, status_word, stream -> (status, y, z)
+PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BEGIN(12)
+  const Product p = product_of(a[0], a[1], a[2] != Py_None, (int)whole(a[4]), number(a[5]));
+  const auto type = p.x.scalar_type();
+  const Rows res = rows_arg(a[6], "residual", type, p.dev, p.rows, p.No);
+  const Rows y = rows_out(a[7], "y", p.x, p.dev, p.rows, p.No, true);
+  at::Tensor z;
+  void* zp = flat(a[8], "z", type, p.dev, {p.rows, p.N});
+  if (!zp && a[8] == Py_None && truth(a[9])) {
+    z = at::empty({p.rows, p.N}, p.x.options());
+    zp = z.data_ptr();
+  }
+  void* status;
+  status_of(a[10], p.dev, &status);
+  void* s = raw_stream(a[11], p.dev);
+  int st;
+  if (p.grouped) {
+    float* bias = static_cast<float*>(flat(a[3], "bias", at::kFloat, p.dev, {p.dims.E, p.N}));
+    const int32_t* off = static_cast<int32_t*>(flat(a[2], "offsets", at::kInt, p.dev, {p.dims.E + 1}));
+    st = g_calls.grouped(&p.dims, (int32_t)p.rows, p.x.data_ptr(), p.ldx, p.w.data_ptr(), off, bias, y.p, y.ld, zp,
+                         static_cast<int32_t*>(status), s);
+  } else {
+    float* bias = static_cast<float*>(flat(a[3], "bias", at::kFloat, p.dev, {p.N}));
+    st = g_calls.linear(&p.dims, (int32_t)p.rows, p.x.data_ptr(), p.ldx, p.w.data_ptr(), bias, res.p, res.ld, y.p, y.ld,
+                        zp, static_cast<int32_t*>(status), s);
+  }
+  return result(st, {{a[7], &y.t}, {a[8], &z}});
+  END
+}
+
+// dy, x, w, offsets, z, fn, limit, dx, dw, need_dx, need_dw, need_db, ws, status_word, stream
+// -> (status, dx, dw, db)
+PyObject* product_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BEGIN(15)
+  const int fn = (int)whole(a[5]);
+  const Product p = product_of(a[1], a[2], a[3] != Py_None, fn, number(a[6]));
+  const auto type = p.x.scalar_type();
+  if (a[0] == Py_None) throw Bad{PyExc_TypeError, "dy: a CUDA tensor is required"};
+  const Rows dy = rows_arg(a[0], "dy", type, p.dev, p.rows, p.No);
+  void* zp = nullptr;
+  if (fn != MOE_FN_NONE) {
+    if (a[4] == Py_None) throw Bad{PyExc_ValueError, "z: the forward pass's pre-activation is required with this fn"};
+    zp = flat(a[4], "z", type, p.dev, {p.rows, p.N});
+  }
+  const Rows dx = rows_out(a[7], "dx", p.x, p.dev, p.rows, p.dims.K, truth(a[9]));
+  at::Tensor dw, db;
+  void* dwp = flat(a[8], "dw", type, p.dev, p.w.sizes());
+  if (a[8] == Py_None && truth(a[10])) {
+    dw = at::empty(p.w.sizes(), p.w.options());
+    dwp = dw.data_ptr();
+  }
+  const bool want_db = truth(a[11]);
+  if (want_db) db = at::empty(p.w.sizes().slice(0, p.w.dim() - 1), p.x.options().dtype(at::kFloat));
+  Scratch ws;
+  if (fn != MOE_FN_NONE || want_db) ws = scratch(a[12], g_calls.workspace(&p.dims, (int32_t)p.rows), p.x, p.dev);
+  void* status;
+  status_of(a[13], p.dev, &status);
+  void* s = raw_stream(a[14], p.dev);
+  float* dbp = want_db ? db.data_ptr<float>() : nullptr;
+  int st;
+  if (p.grouped) {
+    const int32_t* off = static_cast<int32_t*>(flat(a[3], "offsets", at::kInt, p.dev, {p.dims.E + 1}));
+    st = g_calls.grouped_backward(&p.dims, (int32_t)p.rows, dy.p, dy.ld, p.x.data_ptr(), p.ldx, p.w.data_ptr(), off, zp,
+                                  dx.p, dx.ld, dwp, dbp, ws.p, ws.n, static_cast<int32_t*>(status), s);
+  } else {
+    st = g_calls.linear_backward(&p.dims, (int32_t)p.rows, dy.p, dy.ld, p.x.data_ptr(), p.ldx, p.w.data_ptr(), zp, dx.p,
+                                 dx.ld, dwp, dbp, ws.p, ws.n, static_cast<int32_t*>(status), s);
+  }
+  return result(st, {{a[7], &dx.t}, {a[8], &dw}, {nullptr, &db}});
+  END
+}
+
+// The eight addresses of Calls, in order.
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  BEGIN(8)
+  void* p[8];
+  for (int i = 0; i < 8; ++i) {
+    p[i] = PyLong_AsVoidPtr(a[i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  g_calls.norm = reinterpret_cast<decltype(g_calls.norm)>(p[0]);
+  g_calls.norm_backward = reinterpret_cast<decltype(g_calls.norm_backward)>(p[1]);
+  g_calls.norm_workspace = reinterpret_cast<decltype(g_calls.norm_workspace)>(p[2]);
+  g_calls.linear = reinterpret_cast<decltype(g_calls.linear)>(p[3]);
+  g_calls.linear_backward = reinterpret_cast<decltype(g_calls.linear_backward)>(p[4]);
+  g_calls.grouped = reinterpret_cast<decltype(g_calls.grouped)>(p[5]);
+  g_calls.grouped_backward = reinterpret_cast<decltype(g_calls.grouped_backward)>(p[6]);
+  g_calls.workspace = reinterpret_cast<decltype(g_calls.workspace)>(p[7]);
+  Py_RETURN_NONE;
+  END
+}
+
+PyMethodDef kMethods[] = {
+    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
+    {"norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm)), METH_FASTCALL, nullptr},
+    {"norm_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm_backward)), METH_FASTCALL, nullptr},
+    {"product", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(product)), METH_FASTCALL, nullptr},
+    {"product_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(product_backward)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, kMethods};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&kModule); }

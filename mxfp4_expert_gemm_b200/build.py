@@ -16,6 +16,9 @@ LIB = os.path.join(PKG, "libmoe_mxfp4.so")
 # The same library with every store at a computed offset checked against its buffer
 # (-DMOE_DEBUG_BOUNDS): an out-of-range store is skipped and MOE_ERR_BOUNDS recorded.
 LIB_BOUNDS = os.path.join(PKG, "libmoe_mxfp4_bounds.so")
+# The tensor-argument part of the binding (compiled against this torch and Python).
+MARSHAL_SRC = os.path.join(PKG, "binding", "marshal.cpp")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 NVCC_FLAGS = [
@@ -45,9 +48,33 @@ def up_to_date(lib: str = LIB) -> bool:
     return os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime()
 
 
+def build_marshal(force: bool = False) -> str:
+    """Compile ``_marshal.so`` with the host compiler."""
+    newest = max(os.path.getmtime(f) for f in (MARSHAL_SRC, os.path.join(INCLUDE, "moe_mxfp4.h")))
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
+        return MARSHAL
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wno-deprecated-declarations", MARSHAL_SRC, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=(), bounds: bool = False) -> str:
     """Compile the library (with bounds=True: the bounds-checking build, LIB_BOUNDS)."""
     lib = LIB_BOUNDS if bounds else LIB
+    build_marshal(force and not bounds)
     if bounds:
         extra_flags = (*extra_flags, "-DMOE_DEBUG_BOUNDS")
     if not force and up_to_date(lib):
