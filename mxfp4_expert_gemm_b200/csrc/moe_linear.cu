@@ -628,6 +628,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
     lin_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const LinParams p) {
   using C = SplitCfg<MODE, NB>;
+  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::S * C::STAGE);
@@ -669,6 +670,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
   }
   __syncthreads();
   ptx::tc_fence_after();
+  pdl_wait();   // dz, in a backward call; what came before the call is complete without it
   const uint32_t tmem = *s_tmem;
   const LinTile t = *s_tile;
   const int kb_all = t.ok ? (t.clen + kBK - 1) / kBK : 0;
@@ -892,6 +894,7 @@ template <int MODE, bool SW, bool BF>
 __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ BMaps tm_b, const LinParams p) {
   using C = PairCfg<MODE>;
+  pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* epi = smem + C::S * C::STAGE;
@@ -932,6 +935,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
   build_table<MODE>(p, tab, C::STEP);
   ptx::cluster_sync();   // the peer's copies, commits and arrivals find initialized barriers
   ptx::tc_fence_after();
+  pdl_wait();   // (as in the split kernel)
   const uint32_t tmem = *s_tmem;
   const uint32_t n_items = tab->items;
 
@@ -1215,8 +1219,8 @@ int launch_split_of(const LinArgs& a) {
   if (grid > 0x7fffffff) return -1;
   const dim3 g((unsigned)grid), b(C::THREADS);
   const cudaError_t err = p.splits == 1
-      ? launch_kernel(kern, g, b, C::SMEM, a.stream, false, ma, mb, p)
-      : launch_kernel_cluster(kern, g, b, C::SMEM, a.stream, false, (unsigned)p.splits, ma, mb, p);
+      ? launch_kernel(kern, g, b, C::SMEM, a.stream, a.pdl != 0, ma, mb, p)
+      : launch_kernel_cluster(kern, g, b, C::SMEM, a.stream, a.pdl != 0, (unsigned)p.splits, ma, mb, p);
   return err == cudaSuccess ? 1 : -1;
 }
 
@@ -1285,7 +1289,7 @@ int launch_pair_of(const LinArgs& a) {
   p.n_jt = (a.N + p.nw_max - 1) / p.nw_max;
   const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, p.nw_max)) * p.n_it;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, n);
-  return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, false, 2u, ma, mb, p) ==
+  return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, a.pdl != 0, 2u, ma, mb, p) ==
                  cudaSuccess ? 1 : -1;
 }
 
@@ -1446,6 +1450,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
   constexpr int H = FN == MOE_FN_SWIGLU ? 2 : 1;
   __shared__ int s_t[3];
   __shared__ float s_sum[8][256];
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     int e = 0, r0 = 0, n = 0;
@@ -1519,6 +1524,7 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const ActGradParams p) {
 __global__ void __launch_bounds__(256) sum_chunks_kernel(const ActGradParams p) {
   __shared__ float s_sum[8][32];
   __shared__ int s_first;
+  pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.y;
   int a = 0, b = p.rows;
   bool bad = false;
@@ -1539,6 +1545,7 @@ __global__ void __launch_bounds__(256) sum_chunks_kernel(const ActGradParams p) 
     s_first = 0;
   }
   __syncthreads();
+  pdl_wait();
   // (offsets out of order could count past the rows of `partial`)
   const int first = s_first, n = min((b - a + kChunk - 1) / kChunk, p.chunks - first), c = blockIdx.x * 32 + lane;
   float v = 0.f;
@@ -1589,7 +1596,7 @@ int launch_act_grad(const ActGradArgs& a) {
   }
   if (launch_kernel(kern, grid, dim3(256), 0, a.stream, false, p) != cudaSuccess) return -1;
   if (!a.db) return 1;
-  if (launch_kernel(sum_chunks_kernel, dim3((unsigned)((a.N + 31) / 32), (unsigned)a.E), dim3(256), 0, a.stream, false,
+  if (launch_kernel(sum_chunks_kernel, dim3((unsigned)((a.N + 31) / 32), (unsigned)a.E), dim3(256), 0, a.stream, true,
                     p) != cudaSuccess)
     return -1;
   return 2;

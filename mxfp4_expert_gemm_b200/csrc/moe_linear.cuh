@@ -31,6 +31,9 @@ struct LinArgs {
   void* z;                   // [rows][N] or null
   int32_t* status;
   int32_t inject_timeout;
+  // The kernel before this one in the stream is of the same call (it was launched plainly or so
+  // itself): this one may start its prologue under it.
+  int32_t pdl;
   cudaStream_t stream;
 };
 

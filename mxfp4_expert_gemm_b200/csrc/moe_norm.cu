@@ -409,6 +409,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormParams p) {
 // are read from there twice, which keeps the registers for the sums.  D = 0: loaded in place.
 template <class DT, int VEC, int NV, int R, int D, bool LAYER>
 __global__ void __launch_bounds__(VEC < 4 ? 1024 : 576) norm_backward_kernel(const NormParams p) {
+  pdl_trigger();
   __shared__ __align__(16) float s_red[2 * R * 32];
   extern __shared__ float4 s_dyn[];   // the ring, then the block's column sums (2 d floats)
   const int threads = blockDim.x * blockDim.y, self = threadIdx.y * blockDim.x + threadIdx.x;
@@ -642,6 +643,7 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const NormParams p) {
 // dw and db: the rows of `partial` added up; 32 warps take every 32nd row, then meet in order.
 __global__ void __launch_bounds__(1024) norm_reduce_kernel(const NormParams p) {
   __shared__ float s_sum[32][32];
+  pdl_wait();   // `partial`
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;   // of [dw | db]
   float v = 0.f;
@@ -775,7 +777,7 @@ int backward_vec(const NormArgs& a) {
       return -1;
   }
   if (!p.partial) return n;
-  if (launch_kernel(norm_reduce_kernel, dim3((unsigned)(((a.layer ? 2 : 1) * (int64_t)a.d + 31) / 32)), dim3(1024), 0, a.stream, false,
+  if (launch_kernel(norm_reduce_kernel, dim3((unsigned)(((a.layer ? 2 : 1) * (int64_t)a.d + 31) / 32)), dim3(1024), 0, a.stream, g != 0,
                     p) != cudaSuccess)
     return -1;
   return n + 1;

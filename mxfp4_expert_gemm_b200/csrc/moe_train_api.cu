@@ -166,6 +166,7 @@ moe_status backward(const moe_linear_dims* dm, int32_t rows, bool grouped, const
   a.tok = dz;
   a.ld_tok = ld_dz;
   a.inject_timeout = moe::take_injected_timeout();
+  a.pdl = launches > 0;
   if (dx) {
     a.mode = moe::kInputGrad;
     a.other = w;
@@ -175,6 +176,7 @@ moe_status backward(const moe_linear_dims* dm, int32_t rows, bool grouped, const
     if (n < 0) return MOE_ERR_CUDA;
     launches += n;
     a.inject_timeout = 0;
+    a.pdl = 1;
   }
   if (dw) {
     a.mode = moe::kWeightGrad;
