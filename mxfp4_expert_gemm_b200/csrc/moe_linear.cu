@@ -10,9 +10,8 @@
 // The transposed operands are read as they lie in memory, as MN-major operands.  Token rows on
 // N rather than M: a ragged expert's last tile then takes an MMA as narrow as its rows (in
 // steps of 16), where a tile on M would always pay 128 rows, and a decode step's few tokens
-// take an N of 16 under a weight tile of 128 rows that streams through once.  Features on the
-// lanes: a warp's 32 lanes store 32 consecutive values of one output row, so any row can be
-// left out and no shared-memory transpose is needed.
+// take an N of 16 under a weight tile of 128 rows that streams through once; and any row can be
+// left out of the stores.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <algorithm>
@@ -30,7 +29,7 @@ constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s: a stuck pipeline, not a sl
 constexpr int kBK = 64;                       // contraction values per stage (a 128-byte row)
 
 struct LinParams {
-  int32_t rows, E, bf16, fn;
+  int32_t rows, E, fn;
   int32_t I;             // extent of i (columns of out)
   int32_t J;             // extent of j (kWeightGrad: N; else the expert's rows)
   int32_t C;             // extent of c (kWeightGrad: the expert's rows)
@@ -156,9 +155,8 @@ __device__ __forceinline__ int tile_width(int cnt, int nt, int step) {
 }
 
 // Tile `item` of a forward or input-gradient product, found by one warp (E <= 256: 8 experts
-// per lane).  Tiles run expert by expert; within an expert, JFAST: its token tiles run
-// fastest (CTAs that start together then share a weight tile in L2), else its i tiles.
-template <bool JFAST>
+// per lane).  Tiles run expert by expert; within an expert its token tiles run fastest (CTAs that
+// start together then share a weight tile in L2).
 __device__ __forceinline__ LinTile find_row_tile(const LinParams& p, uint32_t item, int step, int iw) {
   const int lane = threadIdx.x & 31;
   LinTile t;
@@ -168,8 +166,7 @@ __device__ __forceinline__ LinTile find_row_tile(const LinParams& p, uint32_t it
   if (!p.offsets) {
     const int nt = (p.rows + p.nw_max - 1) / p.nw_max, w = tile_width(p.rows, nt, step);
     if (item < (uint32_t)nt * (uint32_t)p.n_it) {
-      const int jt = JFAST ? item % (uint32_t)nt : item / (uint32_t)p.n_it;
-      const int it = JFAST ? item / (uint32_t)nt : item % (uint32_t)p.n_it;
+      const int it = item / (uint32_t)nt, jt = item - (uint32_t)it * nt;
       t.ok = 1;
       t.e = 0;
       t.i0 = it * iw;
@@ -226,7 +223,7 @@ __device__ __forceinline__ LinTile find_row_tile(const LinParams& p, uint32_t it
   fc = __shfl_sync(0xffffffffu, fc, src);
   floc = __shfl_sync(0xffffffffu, floc, src);
   const int nt = (fc + p.nw_max - 1) / p.nw_max, w = tile_width(fc, nt, step);
-  const int jt = JFAST ? floc % nt : floc / p.n_it, it = JFAST ? floc / nt : floc % p.n_it;
+  const int it = floc / nt, jt = floc - it * nt;
   t.ok = 1;
   t.e = fe;
   t.i0 = it * iw;
@@ -261,10 +258,10 @@ __device__ __forceinline__ LinTile find_weight_tile(const LinParams& p, uint32_t
   return t;
 }
 
-template <int MODE, bool JFAST>
+template <int MODE>
 __device__ __forceinline__ LinTile find_tile(const LinParams& p, uint32_t item, int step, int iw) {
   if (MODE == kWeightGrad) return find_weight_tile(p, item, step, iw);
-  return find_row_tile<JFAST>(p, item, step, iw);
+  return find_row_tile(p, item, step, iw);
 }
 
 // The experts' row ranges and tiles, kept in shared memory by kernels that take many tiles.
@@ -665,7 +662,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
     ptx::tc_fence_before();
   }
   if (warp == 2) {
-    const LinTile t = find_tile<MODE, true>(p, item, 16, SW ? 64 : 128);
+    const LinTile t = find_tile<MODE>(p, item, 16, SW ? 64 : 128);
     if (lane == 0) *s_tile = t;
   }
   __syncthreads();
@@ -1165,7 +1162,6 @@ LinParams params_of(const LinArgs& a, int iw) {
   const int No = a.fn == MOE_FN_SWIGLU ? a.N / 2 : a.N;
   p.rows = a.rows;
   p.E = a.E;
-  p.bf16 = a.bf16;
   p.fn = a.fn;
   p.limit = a.limit;
   p.I = a.mode == kForward ? No : a.K;
@@ -1392,7 +1388,7 @@ __device__ __forceinline__ bool find_chunk(const ActGradParams& p, int q, int& e
   lp.nw_max = kChunk;
   lp.C = 0;
   lp.status = p.status;
-  const LinTile t = find_row_tile<true>(lp, q, kChunk, 0);
+  const LinTile t = find_row_tile(lp, q, kChunk, 0);
   e = t.e;
   r0 = t.j0;
   n = t.nj;
