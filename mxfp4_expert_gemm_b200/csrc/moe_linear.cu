@@ -595,29 +595,27 @@ __device__ __forceinline__ void lane_bias(const LinParams& p, const LinTile& t, 
 
 // ------------------------------------------------------------------------------ split kernel
 // One CTA (or a cluster of `splits` CTAs that share a tile's contraction) per output tile of
-// 128 i x at most NB j (SwiGLU: 64 gate and the matching 64 up features).
+// 128 i x at most NB j (SwiGLU: 64 gate and the matching 64 up features), two CTAs per SM.
 template <int MODE, int NB>
 struct SplitCfg {
   static constexpr bool A_MN = MODE != kForward, B_MN = MODE == kWeightGrad;
   static constexpr int A_PANEL = 128 * 128;             // 128 i x 64 c of 2 bytes
-  static constexpr int B_BOX = NB < 64 ? NB : 64;       // j per copy of B
   static constexpr int B_BYTES = NB * 128;
   static constexpr int STAGE = A_PANEL + B_BYTES;
   static constexpr int CPS = 2;                         // CTAs per SM
   static constexpr int S = 108 * 1024 / STAGE;
   static constexpr int TMEM_COLS = NB;
   // The stages are reused: the tile's fp32 partials, the received ones (splits x whole groups of
-  // 8 columns: at most 7 more columns per split), the epilogue's buffer.  128-wide tiles leave no room for the first two.
-  static constexpr bool SPLIT = NB <= 64;
-  static constexpr int SEND_BYTES = SPLIT ? NB * 512 : 0, RED_BYTES = SPLIT ? (NB + 32) * 512 : 0;
+  // 8 columns: at most 7 more columns per split), the epilogue's buffer.
+  static constexpr int SEND_BYTES = NB * 512, RED_BYTES = (NB + 32) * 512;
   static constexpr int EPI_OFF = SEND_BYTES + RED_BYTES;
   static constexpr int BAR_BYTES = 8 * (2 * S + 3) + 64;
   static constexpr int SMEM = S * STAGE + BAR_BYTES + 1024 /* align slack */;
   static constexpr int THREADS = 32 * 6;                // producer, MMA, four epilogue warps
   static_assert(EPI_OFF + kEpiBytes <= S * STAGE, "the partial tile and the epilogue's buffer fit the stages");
-  static_assert(!SPLIT || EPI_OFF + 32 * 512 <= S * STAGE, "a sum's reads past its share stay in the stages");
+  static_assert(EPI_OFF + 32 * 512 <= S * STAGE, "a sum's reads past its share stay in the stages");
   static_assert((SMEM + 1024) * CPS <= 228 * 1024, "shared memory of the co-resident CTAs");
-  static_assert((NB == 32 || NB == 64 || NB == 128) && (!B_MN || NB % 64 == 0), "tile width");
+  static_assert((NB == 32 || NB == 64) && (!B_MN || NB % 64 == 0), "tile width");
 };
 
 template <int MODE, bool SW, int NB, bool BF>
@@ -638,8 +636,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
   LinTile* s_tile = reinterpret_cast<LinTile*>(s_tmem + 2);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr bool SPLIT = C::SPLIT;
-  const int S = SPLIT ? p.splits : 1;
+  const int S = p.splits;
   const int rank = S > 1 ? (int)ptx::cluster_ctarank() : 0;
   const uint32_t item = blockIdx.x / (unsigned)S;
 
@@ -672,7 +669,6 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
   const LinTile t = *s_tile;
   const int kb_all = t.ok ? (t.clen + kBK - 1) / kBK : 0;
   const int kb0 = (int)((int64_t)rank * kb_all / S), kb1 = (int)((int64_t)(rank + 1) * kb_all / S);
-  const int nbox = (t.nw + C::B_BOX - 1) / C::B_BOX;   // copies of B per stage
 
   if (warp == 0) {
     // ---------------------------------------------------------------- producer
@@ -690,7 +686,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
       if (ptx::elect_one()) {
         uint8_t* a = smem + s * C::STAGE;
         uint8_t* b = a + C::A_PANEL;
-        ptx::mbar_arrive_expect_tx(&full[s], C::A_PANEL + nbox * C::B_BOX * 128);
+        ptx::mbar_arrive_expect_tx(&full[s], C::STAGE);
         const int c = kb * kBK;
         if (MODE == kForward) {
           if (SW) ptx::tma_load_3d(a, &tm_a, c, t.i0, 2 * t.e, &full[s]);
@@ -703,10 +699,9 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
           const int d1 = tail_shift(t.clen - c), d2 = t.c0 + c;
 #pragma unroll
           for (int h = 0; h < 2; ++h) ptx::tma_load_3d(a + h * 8192, &tm_a, t.i0 + 64 * h, d1, d2, &full[s]);
-          for (int h = 0; h < nbox; ++h) ptx::tma_load_3d(b + h * 8192, &tm_b, t.j0 + 64 * h, d1, d2, &full[s]);
+          ptx::tma_load_3d(b, &tm_b, t.j0, d1, d2, &full[s]);
         } else {
-          for (int h = 0; h < nbox; ++h)
-            ptx::tma_load_2d(b + h * C::B_BOX * 128, &tm_b, c, t.j0 + C::B_BOX * h, &full[s]);
+          ptx::tma_load_2d(b, &tm_b, c, t.j0, &full[s]);
         }
       }
       __syncwarp();
@@ -774,7 +769,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
 
   __syncthreads();
   if (*s_abort && threadIdx.x == 0) set_status(p.status, MOE_ERR_TIMEOUT);
-  if (SPLIT && S > 1) {
+  if (S > 1) {
     // The cluster's partial tiles meet over distributed shared memory: CTA r finishes its share
     // of the columns, whose partials every CTA sends it by one bulk copy (loads or stores by the
     // threads took up to 30 us here).  The sum runs in rank order, so that it does not depend
@@ -1088,6 +1083,127 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
   }
 }
 
+// ------------------------------------------------------------------------------ token kernel
+// A dense forward product of at most 16 rows: nothing but the weights' stream, where the set-up of
+// the tiles (tensor memory, barriers, the cluster's join) took most of the time.  A block takes 16
+// output features (SwiGLU: 8 gate and the 8 up), its 8 warps share the contraction in steps of 32,
+// each lane loads 16 bytes of two weight rows and of NT token rows straight into the fragments of
+// m16n8k16 MMAs, U steps at a time (what the registers of two blocks an SM hold; 4 steps at one
+// token column took 5.9 us for 4096 x 4096, 6 took 6.7, 8 take 5.5), and the warps' sums meet in
+// shared memory in warp order.  Lane l / 4 has a row, lane l % 4 the values 8 (l % 4) .. + 7 of a
+// step: the first half of them stands for the fragments' k 2 (l % 4), + 1, + 8, + 9 of one MMA, the
+// second half for the next; A and B permute k alike, which a sum does not see.
+struct TokenParams {
+  int32_t M, K, N, I, fn;
+  float limit;
+  const uint16_t* x;
+  int64_t ldx;
+  const uint16_t* w;
+  const float* bias;
+  const uint16_t* residual;
+  int64_t ld_res;
+  uint16_t* y;
+  int64_t ldy;
+  uint16_t* z;
+};
+
+template <bool BF>
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if (BF)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <bool SW, int NT, bool BF>
+__global__ void __launch_bounds__(256, 2) lin_token_kernel(const TokenParams p) {
+    constexpr int U = NT == 1 ? 8 : 4, TOK = 8 * NT;
+  __shared__ float s_sum[8][16][TOK + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int f0 = blockIdx.x * (SW ? 8 : 16);
+  const int rows = SW ? p.I : p.N;                     // output features
+  const bool has0 = f0 + g < rows, has1 = SW ? has0 : f0 + 8 + g < rows;
+  const uint16_t* w0 = p.w + (int64_t)(has0 ? f0 + g : 0) * p.K;
+  const uint16_t* w1 = p.w + (int64_t)(has1 ? (SW ? p.I + f0 + g : f0 + 8 + g) : 0) * p.K;
+  float c[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) c[t][r] = 0.f;
+  const int steps = (p.K + 31) / 32;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int s0 = warp; s0 < steps; s0 += 8 * U) {
+    uint4 a0[U], a1[U], b[U][NT];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int k = 32 * (s0 + 8 * i) + 8 * q;         // (K is a multiple of 8)
+      const bool in = k < p.K;
+      a0[i] = in && has0 ? __ldg(reinterpret_cast<const uint4*>(w0 + k)) : zero;
+      a1[i] = in && has1 ? __ldg(reinterpret_cast<const uint4*>(w1 + k)) : zero;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+        b[i][t] = in && 8 * t + g < p.M ? __ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)(8 * t + g) * p.ldx + k)) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma_16816<BF>(c[t], a0[i].x, a1[i].x, a0[i].y, a1[i].y, b[i][t].x, b[i][t].y);
+        mma_16816<BF>(c[t], a0[i].z, a1[i].z, a0[i].w, a1[i].w, b[i][t].z, b[i][t].w);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    s_sum[warp][g][8 * t + 2 * q] = c[t][0];
+    s_sum[warp][g][8 * t + 2 * q + 1] = c[t][1];
+    s_sum[warp][g + 8][8 * t + 2 * q] = c[t][2];
+    s_sum[warp][g + 8][8 * t + 2 * q + 1] = c[t][3];
+  }
+  __syncthreads();
+  constexpr int F = SW ? 8 : 16;
+  for (int i = threadIdx.x; i < F * TOK; i += 256) {
+    const int f = i % F, tok = i / F, col = f0 + f;    // a token's features side by side
+    if (col >= rows || tok >= p.M) continue;
+    float v = 0.f, u = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      v += s_sum[w][f][tok];
+      if (SW) u += s_sum[w][f + 8][tok];
+    }
+    if (p.bias) {
+      v += __ldg(p.bias + col);
+      if (SW) u += __ldg(p.bias + p.I + col);
+    }
+    if (p.z) {
+      uint16_t* z = p.z + (int64_t)tok * p.N + col;
+      z[0] = to16<BF>(v);
+      if (SW) z[p.I] = to16<BF>(u);
+    }
+    float y = v, other = 0.f;
+    if (SW) {
+      y = swiglu(v, u, p.limit);
+    } else {
+      switch (p.fn) {
+        case MOE_FN_RELU: y = act_fn<MOE_FN_RELU>(v); break;
+        case MOE_FN_GELU: act_pair<MOE_FN_GELU>(y, other); break;
+        case MOE_FN_GELU_TANH: y = act_fn<MOE_FN_GELU_TANH>(v); break;
+        case MOE_FN_SILU: y = act_fn<MOE_FN_SILU>(v); break;
+      }
+    }
+    if (p.residual) y += from16<BF>(p.residual[(int64_t)tok * p.ld_res + col]);
+    p.y[(int64_t)tok * p.ldy + col] = to16<BF>(y);
+  }
+}
+
 // ------------------------------------------------------------------------------ host side
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -1196,7 +1312,7 @@ template <int MODE, bool SW, int NB, bool BF>
 int launch_split_of(const LinArgs& a) {
   using C = SplitCfg<MODE, NB>;
   CUtensorMap ma, mb;
-  if (!a_map(a, &ma) || !b_map(a, C::B_BOX, &mb)) return -1;
+  if (!a_map(a, &ma) || !b_map(a, NB, &mb)) return -1;
   LinParams p = params_of(a, SW ? 64 : 128);
   p.nw_max = NB;
   p.n_jt = (a.N + NB - 1) / NB;
@@ -1207,7 +1323,7 @@ int launch_split_of(const LinArgs& a) {
   // SM (128 x 2880 x 2880, 46 tiles: 12.7 us with 3, 19.4 us with 6: the clusters then queue).
   const int64_t blocks = MODE == kWeightGrad ? (a.rows / (a.offsets ? a.E : 1) + kBK - 1) / kBK : (p.C + kBK - 1) / kBK;
   const int64_t s = std::min<int64_t>(5 * (int64_t)multiprocessors() / (4 * tiles), blocks / 5);
-  p.splits = C::SPLIT ? (int)std::max<int64_t>(1, std::min<int64_t>(s, 4)) : 1;
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(s, 4));
   auto kern = lin_split_kernel<MODE, SW, NB, BF>;
   static std::atomic<uint64_t> done{0};
   if (!allow_smem(kern, C::SMEM, done)) return -1;
@@ -1298,6 +1414,33 @@ int launch_split(const LinArgs& a) {
   return a.bf16 ? launch_split_of<MODE, SW, NB, true>(a) : launch_split_of<MODE, SW, NB, false>(a);
 }
 
+template <bool SW, int NT>
+int launch_token(const LinArgs& a) {
+  TokenParams p = {};
+  p.M = a.rows;
+  p.K = a.K;
+  p.N = a.N;
+  p.I = SW ? a.N / 2 : a.N;
+  p.fn = a.fn;
+  p.limit = a.limit;
+  p.x = static_cast<const uint16_t*>(a.tok);
+  p.ldx = a.ld_tok;
+  p.w = static_cast<const uint16_t*>(a.other);
+  p.bias = a.bias;
+  p.residual = static_cast<const uint16_t*>(a.residual);
+  p.ld_res = a.ld_res;
+  p.y = static_cast<uint16_t*>(a.out);
+  p.ldy = a.ld_out;
+  p.z = static_cast<uint16_t*>(a.z);
+  auto kern = a.bf16 ? lin_token_kernel<SW, NT, true> : lin_token_kernel<SW, NT, false>;
+  const int f = SW ? 8 : 16;
+  return launch_kernel(kern, dim3((unsigned)((p.I + f - 1) / f)), dim3(256), 0, a.stream, false, p) == cudaSuccess ? 1 : -1;
+}
+template <bool SW>
+int launch_tokens(const LinArgs& a) {
+  return a.rows <= 8 ? launch_token<SW, 1>(a) : launch_token<SW, 2>(a);
+}
+
 // Tiles of 256 x 256 that the product makes (on average over the experts' counts).
 int64_t pair_tiles(const LinArgs& a) {
   constexpr int nw = 256;
@@ -1311,33 +1454,32 @@ int64_t pair_tiles(const LinArgs& a) {
 }  // namespace
 
 int launch_linear(const LinArgs& a) {
-  const int64_t per = a.rows / (a.offsets ? a.E : 1);   // rows an expert, on average
-  const bool narrow = per <= 32;                        // the weights' stream is the work
   const bool swiglu = a.mode == kForward && a.fn == MOE_FN_SWIGLU;
-  // CTA pairs once their tiles fill about half of the SMs (fewer: smaller tiles on more SMs).
+  // A few tokens: the kernel without tiles, until its many blocks cost more than the tiles' set-up.
+  // Times in us, this kernel against the split tiles, weights K x N: 1 row 2880 x 2880 4.7 : 9.0,
+  // 4096 x 16384 24 : 28, 2880 x 32768 36 : 33; 16 rows 2880 x 2880 6.3 : 9.2, 8192 x 8192 28 : 30,
+  // 4096 x 16384 32 : 28; 24 rows 2880 x 2880 12 : 9.3.
+  if (a.mode == kForward && !a.offsets && a.rows <= 16 && a.N <= (a.rows <= 8 ? 16384 : 8192))
+    return swiglu ? launch_tokens<true>(a) : launch_tokens<false>(a);
+  const bool narrow = a.rows / (a.offsets ? a.E : 1) <= 32;   // rows an expert: the weights' stream is the work
+  // CTA pairs once their tiles fill about half of the SMs; fewer tiles: smaller ones on more SMs,
+  // with clusters that share a contraction.
   const bool pair = pair_tiles(a) >= multiprocessors() / 4 && (a.mode == kWeightGrad || !narrow);
-  // 128-wide tiles once they alone fill the SMs, else 64-wide ones whose contraction clusters share.
-  const bool wide = 4 * pair_tiles(a) >= multiprocessors();
   switch (a.mode) {
     case kForward:
       if (swiglu)
         return pair     ? launch_pair<kForward, true>(a)
                : narrow ? launch_split<kForward, true, 32>(a)
-               : wide   ? launch_split<kForward, true, 128>(a)
                         : launch_split<kForward, true, 64>(a);
       return pair     ? launch_pair<kForward>(a)
              : narrow ? launch_split<kForward, false, 32>(a)
-             : wide   ? launch_split<kForward, false, 128>(a)
                       : launch_split<kForward, false, 64>(a);
     case kInputGrad:
       return pair     ? launch_pair<kInputGrad>(a)
              : narrow ? launch_split<kInputGrad, false, 32>(a)
-             : wide   ? launch_split<kInputGrad, false, 128>(a)
                       : launch_split<kInputGrad, false, 64>(a);
     default:
-      return pair ? launch_pair<kWeightGrad>(a)
-             : wide ? launch_split<kWeightGrad, false, 128>(a)
-                    : launch_split<kWeightGrad, false, 64>(a);
+      return pair ? launch_pair<kWeightGrad>(a) : launch_split<kWeightGrad, false, 64>(a);
   }
 }
 

@@ -28,6 +28,13 @@ FORWARD = [
     (17, 200, 336, "swiglu", HF, True, True, True),
     (32, 1024, 4096, "gelu_tanh", BF, True, False, True),
     (33, 320, 64, "gelu", BF, False, True, False),
+    (1, 136, 16392, "none", BF, True, False, False),
+    (8, 40, 16384, "silu", HF, True, True, True),
+    (16, 104, 8192, "swiglu", BF, True, True, True),
+    (9, 104, 8208, "swiglu", BF, False, False, True),
+    (9, 4104, 1552, "swiglu", HF, False, True, True),
+    (24, 2880, 200, "relu", BF, True, False, False),
+    (8, 65536, 16, "gelu", BF, True, False, True),
     (100, 1000, 24, "gelu", HF, True, True, True),
     (129, 136, 1288, "none", BF, True, False, True),
     (257, 2880, 320, "swiglu", BF, False, False, True),
@@ -60,10 +67,11 @@ def test_linear_forward(M, K, N, fn, dt, bias, residual, want_z):
     assert torch.equal(again[0] if want_z else again, y)
 
 
-def test_linear_strided_rows_and_residual_in_place():
+@pytest.mark.parametrize("M", [3, 20, 77])
+def test_linear_strided_rows_and_residual_in_place(M):
     """Rows of wider buffers, and y written over the residual it adds."""
     g = generator(5)
-    M, K, N = 77, 264, 144
+    K, N = 264, 144
     xb, yb = normal(g, M, K + 56), normal(g, M, N + 24)
     x, y = xb[:, 16:16 + K], yb[:, 8:8 + N]
     w = normal(g, N, K, std=0.1)
@@ -73,6 +81,14 @@ def test_linear_strided_rows_and_residual_in_place():
     assert got.data_ptr() == y.data_ptr()
     assert_close(y, yr, ey)
     assert torch.equal(yb[:, :8], before[:, :8]) and torch.equal(yb[:, 8 + N:], before[:, 8 + N:])
+
+
+def test_swiglu_rows_come_in_pairs_of_eight():
+    """N = 1544 is a multiple of 8 but not of 16: half of it is no whole 16-byte row."""
+    x, w = torch.ones(9, 4104, dtype=HF, device="cuda"), torch.ones(1544, 4104, dtype=HF, device="cuda")
+    with pytest.raises(moe.MoeError) as e:
+        moe.moe_linear(x, w, fn="swiglu")
+    assert e.value.status == moe.MOE_ERR_UNSUPPORTED_SHAPE
 
 
 def test_linear_clamp_and_large_values():
