@@ -429,15 +429,27 @@ __device__ __forceinline__ void store_rows(const LinParams& p, const uint8_t* bu
   }
 }
 
-template <int W>
-__device__ __forceinline__ void load_rows(uint8_t* buf, int pitch, const uint16_t* src, int64_t ld, int n, int lim,
-                                          int th) {
-  constexpr int V = W / 8;
+// This thread's pieces of the residual's 32 rows from col0 on.  They are fetched a step ahead, in
+// registers, while the columns before them are finished: read where they were added, one after
+// another, they made 16384 x 64 x 5760 258 us for 61 without a residual.
+template <bool SW>
+__device__ __forceinline__ void fetch_residual(const LinParams& p, const LinTile& t, int col0, int th, uint4 (&res)[4]) {
+  constexpr int V = SW ? 8 : 16;        // pieces per row
   const int v = th % V;
-  if (8 * v >= lim) return;
+  if (!p.residual || col0 >= t.nj || 8 * v >= p.I - t.i0) return;
+  const uint16_t* src = p.residual + (int64_t)(t.j0 + col0) * p.ld_res + t.i0 + 8 * v;
 #pragma unroll
-  for (int c = th / V; c < 32; c += 128 / V)
-    if (c < n) *reinterpret_cast<uint4*>(buf + c * pitch + 16 * v) = *reinterpret_cast<const uint4*>(src + c * ld + 8 * v);
+  for (int k = 0; k < V / 4; ++k) {
+    const int c = th / V + 128 / V * k;
+    if (c < t.nj - col0) res[k] = *reinterpret_cast<const uint4*>(src + c * p.ld_res);
+  }
+}
+template <bool SW>
+__device__ __forceinline__ void place_residual(uint8_t* buf, int pitch, int th, const uint4 (&res)[4]) {
+  constexpr int V = SW ? 8 : 16;
+#pragma unroll
+  for (int k = 0; k < V / 4; ++k)
+    *reinterpret_cast<uint4*>(buf + (th / V + 128 / V * k) * pitch + 16 * (th % V)) = res[k];
 }
 
 // Column groups G0 .. G0 + NG - 1 of the fragments into the buffer (row 8 g + k, this warp's 32
@@ -486,7 +498,7 @@ __device__ __forceinline__ void swiglu_half(const LinParams& p, float (&v)[32], 
 
 template <int FN, bool BF>
 __device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t, float (&v)[32], int col0, int th,
-                                            uint8_t* buf, int bar) {
+                                            uint8_t* buf, int bar, uint4 (&res)[4], int next) {
   const int n = min(32, t.nj - col0);   // valid columns
   const int64_t r0 = t.j0 + col0;
   uint16_t* out = p.out + t.e * p.out_expert + r0 * p.ld_out + t.i0;
@@ -531,7 +543,8 @@ __device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t
     group_sync(bar);
     const int at = 64 * (q & 1);
     if (p.residual) {
-      load_rows<64>(buf + 32 * kPitchSw, kPitchSw, p.residual + r0 * p.ld_res + t.i0, p.ld_res, n, lim, th);
+      place_residual<true>(buf + 32 * kPitchSw, kPitchSw, th, res);
+      fetch_residual<true>(p, t, next, th, res);
       group_sync(bar);
       if (up) add_frag<BF, 2, 2>(buf + 32 * kPitchSw, kPitchSw, at, v);
       else add_frag<BF, 0, 2>(buf + 32 * kPitchSw, kPitchSw, at, v);
@@ -544,7 +557,8 @@ __device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t
 #pragma unroll
     for (int c = 0; c < 32; c += 2) act_pair<FN>(v[c], v[c + 1]);
     if (p.residual) {
-      load_rows<128>(buf, kPitch, p.residual + r0 * p.ld_res + t.i0, p.ld_res, n, lim, th);
+      place_residual<false>(buf, kPitch, th, res);
+      fetch_residual<false>(p, t, next, th, res);
       group_sync(bar);
       add_frag<BF, 0, 4>(buf, kPitch, 64 * q, v);   // (a warp reads and then overwrites its own values alone)
       __syncwarp();
@@ -556,10 +570,12 @@ __device__ __forceinline__ void finish_cols(const LinParams& p, const LinTile& t
 }
 
 // acc: the raw accumulator values; bias: of this thread's four accumulator lanes; th: the thread's
-// number in its group, 32 q + lane.
+// number in its group, 32 q + lane; res: the residual's pieces of these columns, then those from
+// column `next` on.
 template <int MODE, bool SW, bool BF>
 __device__ __forceinline__ void finish(const LinParams& p, const LinTile& t, const uint32_t (&acc)[32],
-                                       const float (&bias)[4], int col0, int th, uint8_t* buf, int bar) {
+                                       const float (&bias)[4], int col0, int th, uint8_t* buf, int bar,
+                                       uint4 (&res)[4], int next) {
   if (col0 >= t.nj) return;   // (the same for the whole group)
   float v[32];
 #pragma unroll
@@ -567,16 +583,16 @@ __device__ __forceinline__ void finish(const LinParams& p, const LinTile& t, con
     v[c] = __uint_as_float(acc[c]);
     if (MODE == kForward) v[c] += bias[2 * (c >> 4) + ((c >> 1) & 1)];
   }
-  if (SW) return finish_cols<MOE_FN_SWIGLU, BF>(p, t, v, col0, th, buf, bar);
+  if (SW) return finish_cols<MOE_FN_SWIGLU, BF>(p, t, v, col0, th, buf, bar, res, next);
   if (MODE == kForward) {
     switch (p.fn) {
-      case MOE_FN_RELU: return finish_cols<MOE_FN_RELU, BF>(p, t, v, col0, th, buf, bar);
-      case MOE_FN_GELU: return finish_cols<MOE_FN_GELU, BF>(p, t, v, col0, th, buf, bar);
-      case MOE_FN_GELU_TANH: return finish_cols<MOE_FN_GELU_TANH, BF>(p, t, v, col0, th, buf, bar);
-      case MOE_FN_SILU: return finish_cols<MOE_FN_SILU, BF>(p, t, v, col0, th, buf, bar);
+      case MOE_FN_RELU: return finish_cols<MOE_FN_RELU, BF>(p, t, v, col0, th, buf, bar, res, next);
+      case MOE_FN_GELU: return finish_cols<MOE_FN_GELU, BF>(p, t, v, col0, th, buf, bar, res, next);
+      case MOE_FN_GELU_TANH: return finish_cols<MOE_FN_GELU_TANH, BF>(p, t, v, col0, th, buf, bar, res, next);
+      case MOE_FN_SILU: return finish_cols<MOE_FN_SILU, BF>(p, t, v, col0, th, buf, bar, res, next);
     }
   }
-  finish_cols<MOE_FN_NONE, BF>(p, t, v, col0, th, buf, bar);
+  finish_cols<MOE_FN_NONE, BF>(p, t, v, col0, th, buf, bar, res, next);
 }
 
 // The biases of this thread's accumulator lanes (SwiGLU: lanes 0-63 the gate's, 64-127 the up's).
@@ -752,6 +768,8 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
     const int q = warp & 3, row = 32 * q + lane;
     const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
     const bool have = kb1 > kb0;
+    uint4 res[4] = {};
+    if (MODE == kForward && S == 1 && t.ok) fetch_residual<SW>(p, t, 0, row, res);
     const bool ready = ptx::mbar_wait_bounded(accf, 0, s_abort, kWaitNs);
     if (!ptx::bar_or<1, 128>(!ready) && t.ok) {
       ptx::tc_fence_after();
@@ -761,7 +779,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
         for (int c0 = 0; c0 < t.nw; c0 += 32) {
           uint32_t v[32];
           load_acc(acc + c0, have, v);
-          finish<MODE, SW, BF>(p, t, v, bias, c0, row, smem + C::EPI_OFF, 2);
+          finish<MODE, SW, BF>(p, t, v, bias, c0, row, smem + C::EPI_OFF, 2, res, c0 + 32);
         }
       }
     }
@@ -810,13 +828,15 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
       __syncwarp();
     }
     if (warp >= 2 && t.ok) {
+      const int c1 = min((rank + 1) * per, t.nj);
+      LinTile part = t;
+      part.nj = c1;
+      uint4 res[4] = {};
+      if (MODE == kForward) fetch_residual<SW>(p, part, rank * per, row, res);
       const bool here = ptx::mbar_wait_cluster_bounded(redf, 0, s_abort, kWaitNs);
       if (!ptx::bar_or<1, 128>(!here)) {
         float bias[4];
         lane_bias<MODE, SW>(p, t, row, bias);
-        const int c1 = min((rank + 1) * per, t.nj);
-        LinTile part = t;
-        part.nj = c1;
         for (int c0 = rank * per; c0 < c1; c0 += 32) {
           // One rank's 32 columns at a time, in straight-line code: a loop over the ranks inside
           // each column ran cold instructions column by column, 17 us for 32 of them.  Columns past
@@ -840,7 +860,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
           }
 #pragma unroll
           for (int c = 0; c < 32; ++c) v[c] = __float_as_uint(sum[c]);
-          finish<MODE, SW, BF>(p, part, v, bias, c0, row, smem + C::EPI_OFF, 2);
+          finish<MODE, SW, BF>(p, part, v, bias, c0, row, smem + C::EPI_OFF, 2, res, c0 + 32);
         }
       } else {
         set_status(p.status, MOE_ERR_TIMEOUT);
@@ -1052,6 +1072,8 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       const bool have = t.clen > 0;
       float bias[4];
       lane_bias<MODE, SW>(p, t, row, bias);
+      uint4 res[4] = {};
+      if (MODE == kForward) fetch_residual<SW>(p, t, 32 * part, row, res);
       const bool ready = !*s_abort && ptx::mbar_wait_bounded(&accf[b2], (uint32_t)(li >> 1) & 1, s_abort, kWaitNs);
       // (one answer for all epilogue warps: another role may raise the abort flag at any time)
       if (ptx::bar_or<1, 32 * C::EPI_WARPS>(!ready)) break;
@@ -1067,7 +1089,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
         uint32_t v[32];
         load_acc(acc + c0, have, v);   // (an expert without rows: never written)
         if (c0 + 64 >= t.nw) release();
-        finish<MODE, SW, BF>(p, t, v, bias, c0, row, epi + kEpiBytes * part, 2 + part);
+        finish<MODE, SW, BF>(p, t, v, bias, c0, row, epi + kEpiBytes * part, 2 + part, res, c0 + 64);
       }
     }
   }
