@@ -1,6 +1,7 @@
 // Matrix products in 16-bit types with fp32 accumulation on tcgen05 (kind::f16): the dense
 // product with bias, activation and residual in its epilogue, the same product grouped by
-// expert over ragged row ranges, and their two gradients.
+// expert over ragged row ranges, and their two gradients.  (A dense forward product of a few rows:
+// warp-level MMAs, lin_token_kernel.)
 //
 // Every product is written as out[j][i] = sum_c A[i][c] B[j][c], with i on the MMA's M (the
 // TMEM lanes) and j on its N (the columns):
