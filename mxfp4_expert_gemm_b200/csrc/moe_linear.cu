@@ -834,8 +834,11 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
       part.nj = c1;
       uint4 res[4] = {};
       if (MODE == kForward) fetch_residual<SW>(p, part, rank * per, row, res);
-      const bool here = ptx::mbar_wait_cluster_bounded(redf, 0, s_abort, kWaitNs);
-      if (!ptx::bar_or<1, 128>(!here)) {
+      // With a flag of its own: every CTA sends whether or not its pipeline timed out, and the copies
+      // into this one have to have landed before the last barrier below lets it and its peers go.
+      volatile int late = 0;
+      ptx::mbar_wait_cluster_bounded(redf, 0, &late, kWaitNs);
+      if (!ptx::bar_or<1, 128>(late || *s_abort)) {
         float bias[4];
         lane_bias<MODE, SW>(p, t, row, bias);
         for (int c0 = rank * per; c0 < c1; c0 += 32) {
