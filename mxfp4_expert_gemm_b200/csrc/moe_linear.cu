@@ -27,6 +27,7 @@ namespace moe {
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s: a stuck pipeline, not a slow one
+constexpr uint64_t kLandNs = 20000000ull;     // 20 ms: copies issued before a timeout have landed
 constexpr int kBK = 64;                       // contraction values per stage (a 128-byte row)
 
 struct LinParams {
@@ -1017,6 +1018,12 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       for (int q = (g > C::S ? g - C::S : 0); q < g; ++q) {
         if (withheld && q == 0) continue;
         ptx::mbar_wait_bounded(&full[q % C::S], (uint32_t)(q / C::S) & 1, &local_abort, kWaitNs);
+      }
+    } else if (stop) {
+      // After a timeout the leader may have stopped at an earlier stage than this CTA, whose last
+      // copies nobody then counts: it stays until they have long landed (they take microseconds).
+      const uint64_t t0 = ptx::globaltimer_ns();
+      while (ptx::globaltimer_ns() - t0 < kLandNs) {
       }
     }
     __syncwarp();
