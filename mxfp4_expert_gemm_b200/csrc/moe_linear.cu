@@ -1547,8 +1547,9 @@ __device__ __forceinline__ float act_grad(float z, float dy) {
     return dy * s * (1.f + z * (1.f - s));
   }
   if (FN == MOE_FN_GELU_TANH) {   // s = (1 + tanh v) / 2, (1 - tanh^2 v) / 2 = 2 s (1 - s)
-    const float s = __fdividef(1.f, 1.f + __expf(-2.f * gelu_arg(z)));
-    return dy * (s + 2.f * z * s * (1.f - s) * 0.79788456f * (1.f + 0.134145f * z * z));
+    // (past 16 the second term is 0: there z^2 may overflow, and infinity times 0 is no slope)
+    const float s = __fdividef(1.f, 1.f + __expf(-2.f * gelu_arg(z))), c = fminf(fmaxf(z, -16.f), 16.f);
+    return dy * (s + 2.f * c * s * (1.f - s) * 0.79788456f * (1.f + 0.134145f * c * c));
   }
   return dy;
 }
