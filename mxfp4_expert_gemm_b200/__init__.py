@@ -507,7 +507,8 @@ def moe_debug_inject_timeout(enable: bool = True) -> None:
 
 
 # ----------------------------------------------------------- norms and 16-bit products, with gradients
-# Checks, allocations and the calls themselves are in binding/marshal.cpp.
+# Checks, allocations and the calls themselves are in binding/marshal.cpp.  With `stream`, the tensors
+# and the scratch that a call makes are that stream's, as under torch.cuda.stream(stream).
 def _handle(stream):
     return None if stream is None else stream.cuda_stream
 
@@ -517,14 +518,6 @@ def _named(name, table, what) -> int:
     if i is None:
         raise ValueError(f"{what}: {name!r}, expected one of {sorted(table)}")
     return i
-
-
-def _scratch_on(stream, nbytes: int, like):
-    """Scratch for a call on a stream that is not the current one: torch's allocator must not hand it
-    on before that stream has passed the call."""
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=like.device)
-    ws.record_stream(stream)
-    return ws
 
 
 def moe_norm(x, w, b=None, kind="rms", eps=1e-5, y=None, want_stats=False, stream=None):
@@ -549,8 +542,6 @@ def moe_norm_backward(dy, x, w, mean, rstd, kind="rms", dres=None, dx=None, need
     k = _named(kind, NORM_KINDS, "kind")
     if need_db is None:
         need_db = k == 1
-    if stream is not None and ws is None and x.dim() == 2:
-        ws = _scratch_on(stream, moe_norm_workspace_bytes(*x.shape), x)
     st, dx, dw, db = _calls().norm_backward(dy, x, w, mean, rstd, k, dres, dx, need_dw, need_db, ws, _handle(stream))
     if st:
         raise MoeError(st, "moe_norm_backward")
@@ -578,12 +569,8 @@ def _forward_product(what, x, w, offsets, bias, fn, limit, residual, y, z, want_
 
 def _backward_product(what, dy, x, w, offsets, z, fn, limit, dx, dw, need_dx, need_dw, need_db, ws, status_word,
                       stream):
-    f = _named(fn, FNS, "fn")
-    if stream is not None and ws is None and x.dim() == 2 and w.dim() in (2, 3):
-        dims = make_linear_dims(x.shape[1], w.shape[-2], w.shape[0] if w.dim() == 3 else 1, x.dtype, fn, limit)
-        ws = _scratch_on(stream, moe_linear_workspace_bytes(dims, x.shape[0]), x)
-    st, dx, dw, db = _calls().product_backward(dy, x, w, offsets, z, f, limit, dx, dw, need_dx, need_dw, need_db, ws,
-                                               status_word, _handle(stream))
+    st, dx, dw, db = _calls().product_backward(dy, x, w, offsets, z, _named(fn, FNS, "fn"), limit, dx, dw, need_dx,
+                                               need_dw, need_db, ws, status_word, _handle(stream))
     if st:
         raise MoeError(st, what)
     return dx, dw, db

@@ -8,6 +8,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -113,12 +114,22 @@ Rows rows_out(PyObject* o, const char* name, const at::Tensor& like, int dev, in
   return r;
 }
 
-void* raw_stream(PyObject* o, int dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-  void* s = PyLong_AsVoidPtr(o);
-  if (PyErr_Occurred()) throw python_error();
-  return s;
-}
+// The call's stream: the current one (None) or a given one, which then is torch's current stream while
+// the call's outputs and scratch are made.  A block of another stream's pool may still be in use by
+// kernels that this one does not wait for, and would go back there while this one still writes it.
+struct Stream {
+  void* raw = nullptr;
+  c10::cuda::OptionalCUDAStreamGuard guard;
+  Stream(PyObject* o, int dev) {
+    if (o == Py_None) {
+      raw = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+      return;
+    }
+    raw = PyLong_AsVoidPtr(o);
+    if (PyErr_Occurred()) throw python_error();
+    guard.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(raw), (c10::DeviceIndex)dev));
+  }
+};
 
 struct Scratch {
   at::Tensor t;
@@ -211,6 +222,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor& x = first_tensor(a[0], "x");
   const int dev = x.get_device(), dt = dtype_of(x, true), kind = (int)whole(a[3]);
   const int64_t T = x.size(0), d = x.size(1), ldx = row_stride(x, "x", T, d);
+  const Stream stream(a[7], dev);
   void* w = flat(a[1], "w", at::kFloat, dev, {d});
   void* b = flat(a[2], "b", at::kFloat, dev, {d});
   const Rows y = rows_out(a[5], "y", x, dev, T, d, true);
@@ -223,7 +235,7 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int st = g_calls.norm(kind, dt, (int32_t)T, (int32_t)d, x.data_ptr(), ldx, static_cast<float*>(w),
                               static_cast<float*>(b), (float)number(a[4]), y.p, y.ld,
                               mean.defined() ? mean.data_ptr<float>() : nullptr,
-                              rstd.defined() ? rstd.data_ptr<float>() : nullptr, raw_stream(a[7], dev));
+                              rstd.defined() ? rstd.data_ptr<float>() : nullptr, stream.raw);
   return result(st, {{a[5], &y.t}, {nullptr, &mean}, {nullptr, &rstd}});
   END
 }
@@ -236,6 +248,7 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int dev = x.get_device(), dt = dtype_of(x, true), kind = (int)whole(a[5]);
   const int64_t T = x.size(0), d = x.size(1), ldx = row_stride(x, "x", T, d);
   if (a[0] == Py_None) throw Bad{PyExc_TypeError, "dy: a CUDA tensor is required"};
+  const Stream stream(a[11], dev);
   const Rows dy = rows_arg(a[0], "dy", type, dev, T, d), dres = rows_arg(a[6], "dres", type, dev, T, d);
   void* w = flat(a[2], "w", at::kFloat, dev, {d});
   void* mean = flat(a[3], "mean", at::kFloat, dev, {T});
@@ -250,7 +263,7 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int st = g_calls.norm_backward(kind, dt, (int32_t)T, (int32_t)d, dy.p, dy.ld, x.data_ptr(), ldx,
                                        static_cast<float*>(w), static_cast<float*>(mean), static_cast<float*>(rstd),
                                        dres.p, dres.ld, dx.p, dx.ld, dw.defined() ? dw.data_ptr<float>() : nullptr,
-                                       db.defined() ? db.data_ptr<float>() : nullptr, ws.p, ws.n, raw_stream(a[11], dev));
+                                       db.defined() ? db.data_ptr<float>() : nullptr, ws.p, ws.n, stream.raw);
   return result(st, {{a[7], &dx.t}, {nullptr, &dw}, {nullptr, &db}});
   END
 }
@@ -283,6 +296,7 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   BEGIN(12)
   const Product p = product_of(a[0], a[1], a[2] != Py_None, (int)whole(a[4]), number(a[5]));
   const auto type = p.x.scalar_type();
+  const Stream stream(a[11], p.dev);
   const Rows res = rows_arg(a[6], "residual", type, p.dev, p.rows, p.No);
   const Rows y = rows_out(a[7], "y", p.x, p.dev, p.rows, p.No, true);
   at::Tensor z;
@@ -293,17 +307,16 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   }
   void* status;
   status_of(a[10], p.dev, &status);
-  void* s = raw_stream(a[11], p.dev);
   int st;
   if (p.grouped) {
     float* bias = static_cast<float*>(flat(a[3], "bias", at::kFloat, p.dev, {p.dims.E, p.N}));
     const int32_t* off = static_cast<int32_t*>(flat(a[2], "offsets", at::kInt, p.dev, {p.dims.E + 1}));
     st = g_calls.grouped(&p.dims, (int32_t)p.rows, p.x.data_ptr(), p.ldx, p.w.data_ptr(), off, bias, y.p, y.ld, zp,
-                         static_cast<int32_t*>(status), s);
+                         static_cast<int32_t*>(status), stream.raw);
   } else {
     float* bias = static_cast<float*>(flat(a[3], "bias", at::kFloat, p.dev, {p.N}));
     st = g_calls.linear(&p.dims, (int32_t)p.rows, p.x.data_ptr(), p.ldx, p.w.data_ptr(), bias, res.p, res.ld, y.p, y.ld,
-                        zp, static_cast<int32_t*>(status), s);
+                        zp, static_cast<int32_t*>(status), stream.raw);
   }
   return result(st, {{a[7], &y.t}, {a[8], &z}});
   END
@@ -317,6 +330,7 @@ PyObject* product_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Product p = product_of(a[1], a[2], a[3] != Py_None, fn, number(a[6]));
   const auto type = p.x.scalar_type();
   if (a[0] == Py_None) throw Bad{PyExc_TypeError, "dy: a CUDA tensor is required"};
+  const Stream stream(a[14], p.dev);
   const Rows dy = rows_arg(a[0], "dy", type, p.dev, p.rows, p.No);
   void* zp = nullptr;
   if (fn != MOE_FN_NONE) {
@@ -336,16 +350,15 @@ PyObject* product_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (fn != MOE_FN_NONE || want_db) ws = scratch(a[12], g_calls.workspace(&p.dims, (int32_t)p.rows), p.x, p.dev);
   void* status;
   status_of(a[13], p.dev, &status);
-  void* s = raw_stream(a[14], p.dev);
   float* dbp = want_db ? db.data_ptr<float>() : nullptr;
   int st;
   if (p.grouped) {
     const int32_t* off = static_cast<int32_t*>(flat(a[3], "offsets", at::kInt, p.dev, {p.dims.E + 1}));
     st = g_calls.grouped_backward(&p.dims, (int32_t)p.rows, dy.p, dy.ld, p.x.data_ptr(), p.ldx, p.w.data_ptr(), off, zp,
-                                  dx.p, dx.ld, dwp, dbp, ws.p, ws.n, static_cast<int32_t*>(status), s);
+                                  dx.p, dx.ld, dwp, dbp, ws.p, ws.n, static_cast<int32_t*>(status), stream.raw);
   } else {
     st = g_calls.linear_backward(&p.dims, (int32_t)p.rows, dy.p, dy.ld, p.x.data_ptr(), p.ldx, p.w.data_ptr(), zp, dx.p,
-                                 dx.ld, dwp, dbp, ws.p, ws.n, static_cast<int32_t*>(status), s);
+                                 dx.ld, dwp, dbp, ws.p, ws.n, static_cast<int32_t*>(status), stream.raw);
   }
   return result(st, {{a[7], &dx.t}, {a[8], &dw}, {nullptr, &db}});
   END
