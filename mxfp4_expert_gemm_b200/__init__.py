@@ -77,7 +77,7 @@ def make_dims(d: int, I: int, E: int, top_k: int, rms_eps: float = 1e-5, swiglu_
 
 
 _lib = None
-_marshal = None   # the compiled part of the binding, bound to _lib
+_marshal = None   # the compiled part of the binding, bound to _lib; loaded by the first call that needs it
 _lock = threading.Lock()
 
 
@@ -89,47 +89,54 @@ def lib():
             if not os.path.exists(LIB_PATH):
                 raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m mxfp4_expert_gemm_b200.build`")
             _lib = load_library(LIB_PATH)
-            _bind(_lib)
     return _lib
 
 
-def _bind(L) -> None:
-    """Point the compiled argument marshalling at a build of the library."""
+def _calls():
+    """The compiled part of the binding.  Published once it is bound: another thread sees either
+    nothing or all of it."""
     global _marshal
     if _marshal is None:
-        path = os.path.join(_PKG, "_marshal.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"{path} is missing: build it with `python -m mxfp4_expert_gemm_b200.build`")
-        spec = importlib.util.spec_from_file_location("_marshal", path)
-        _marshal = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_marshal)
-    _marshal.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib()
+        with _lock:
+            if _marshal is None:
+                path = os.path.join(_PKG, "_marshal.so")
+                if not os.path.exists(path):
+                    raise RuntimeError(f"{path} is missing: build it with `python -m mxfp4_expert_gemm_b200.build`")
+                spec = importlib.util.spec_from_file_location("_marshal", path)
+                m = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(m)
+                _bind(m, _lib)
+                _marshal = m
+    return _marshal
+
+
+def _bind(m, L) -> None:
+    """Point the compiled part at a build of the library."""
+    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
         L.moe_norm, L.moe_norm_backward, L.moe_norm_workspace_bytes, L.moe_linear, L.moe_linear_backward,
         L.moe_grouped_linear, L.moe_grouped_linear_backward, L.moe_linear_workspace_bytes)))
 
 
-def _calls():
-    if _lib is None:
-        lib()
-    return _marshal
+def _use(L) -> None:
+    global _lib
+    with _lock:
+        _lib = L
+        if _marshal is not None:
+            _bind(_marshal, L)
 
 
 @contextlib.contextmanager
 def use_library(path: str):
     """Run the calls inside the block on another build of the library (for example the
     bounds-checking build, libmoe_mxfp4_bounds.so), then switch back."""
-    global _lib
     other = load_library(path)
     prev = lib()
-    with _lock:
-        _lib = other
-        _bind(other)
+    _use(other)
     try:
         yield other
     finally:
-        with _lock:
-            _lib = prev
-            _bind(prev)
+        _use(prev)
 
 
 def load_library(path: str):

@@ -208,6 +208,10 @@ int64_t whole(PyObject* o) {
     PyErr_SetString(PyExc_TypeError, "wrong number of arguments");         \
     return nullptr;                                                        \
   }                                                                        \
+  if (!g_calls.workspace) {                                                \
+    PyErr_SetString(PyExc_RuntimeError, "not bound to a library");         \
+    return nullptr;                                                        \
+  }                                                                        \
   try {
 #define END                                                                \
   } catch (const Bad& b) {                                                 \
@@ -366,11 +370,18 @@ PyObject* product_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // The eight addresses of Calls, in order.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  BEGIN(8)
+  if (n != 8) {
+    PyErr_SetString(PyExc_TypeError, "wrong number of arguments");
+    return nullptr;
+  }
   void* p[8];
   for (int i = 0; i < 8; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
+    if (!p[i]) {
+      PyErr_SetString(PyExc_ValueError, "a null address");
+      return nullptr;
+    }
   }
   g_calls.norm = reinterpret_cast<decltype(g_calls.norm)>(p[0]);
   g_calls.norm_backward = reinterpret_cast<decltype(g_calls.norm_backward)>(p[1]);
@@ -381,7 +392,6 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_calls.grouped_backward = reinterpret_cast<decltype(g_calls.grouped_backward)>(p[6]);
   g_calls.workspace = reinterpret_cast<decltype(g_calls.workspace)>(p[7]);
   Py_RETURN_NONE;
-  END
 }
 
 PyMethodDef kMethods[] = {
