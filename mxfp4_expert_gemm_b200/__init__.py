@@ -13,6 +13,7 @@ import ctypes
 import importlib.util
 import os
 import re
+import sys
 import threading
 
 import torch
@@ -92,6 +93,12 @@ def lib():
     return _lib
 
 
+def marshal_path() -> str:
+    """Where the compiled part of the binding lies: it is good for the torch and Python that it was
+    compiled against, which its name states."""
+    return os.path.join(_PKG, f"_marshal.{sys.implementation.cache_tag}-torch-{torch.__version__}.so")
+
+
 def _calls():
     """The compiled part of the binding.  Published once it is bound: another thread sees either
     nothing or all of it."""
@@ -100,7 +107,7 @@ def _calls():
         lib()
         with _lock:
             if _marshal is None:
-                path = os.path.join(_PKG, "_marshal.so")
+                path = marshal_path()
                 if not os.path.exists(path):
                     raise RuntimeError(f"{path} is missing: build it with `python -m mxfp4_expert_gemm_b200.build`")
                 spec = importlib.util.spec_from_file_location("_marshal", path)

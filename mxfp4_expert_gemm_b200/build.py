@@ -16,9 +16,8 @@ LIB = os.path.join(PKG, "libmoe_mxfp4.so")
 # The same library with every store at a computed offset checked against its buffer
 # (-DMOE_DEBUG_BOUNDS): an out-of-range store is skipped and MOE_ERR_BOUNDS recorded.
 LIB_BOUNDS = os.path.join(PKG, "libmoe_mxfp4_bounds.so")
-# The tensor-argument part of the binding (compiled against this torch and Python).
+# The tensor-argument part of the binding (compiled against this torch and Python, named by them).
 MARSHAL_SRC = os.path.join(PKG, "binding", "marshal.cpp")
-MARSHAL = os.path.join(PKG, "_marshal.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 NVCC_FLAGS = [
@@ -49,16 +48,18 @@ def up_to_date(lib: str = LIB) -> bool:
 
 
 def build_marshal(force: bool = False) -> str:
-    """Compile ``_marshal.so`` with the host compiler."""
+    """Compile the binding's part in C++ with the host compiler."""
+    from mxfp4_expert_gemm_b200 import marshal_path
+    lib = marshal_path()
     newest = max(os.path.getmtime(f) for f in (MARSHAL_SRC, os.path.join(INCLUDE, "moe_mxfp4.h")))
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= newest:
-        return MARSHAL
+    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= newest:
+        return lib
     import sysconfig
 
     import torch
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
-    tmp = MARSHAL + f".tmp{os.getpid()}"
+    tmp = lib + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wno-deprecated-declarations", MARSHAL_SRC, "-o", tmp,
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
            "-I", os.path.join(root, "include"), "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
@@ -67,8 +68,8 @@ def build_marshal(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    os.replace(tmp, lib)
+    return lib
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), bounds: bool = False) -> str:

@@ -93,6 +93,13 @@ def test_a_missing_compiled_part_stops_its_own_calls_only(unloaded, monkeypatch)
     monkeypatch.undo()
 
 
+def test_a_compiled_part_for_another_torch_is_not_loaded(unloaded, monkeypatch):
+    assert isinstance(_refusal(), TypeError)
+    monkeypatch.setattr(moe, "_marshal", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert isinstance(_refusal(), RuntimeError) and "missing" in str(_refusal())
+
+
 def test_another_library_is_bound_too(unloaded):
     """use_library before and after the first product call."""
     for _ in range(2):
