@@ -91,10 +91,15 @@ void* flat(PyObject* o, const char* name, at::ScalarType type, int dev, at::IntA
   return t.data_ptr();
 }
 
-struct Rows {   // a [rows, cols] operand: given, or (where `make`) made here
+struct Rows {   // a [rows, cols] operand: given, or made here
   at::Tensor t;
   void* p = nullptr;
   int64_t ld = 0;
+  void make(const at::Tensor& like, int64_t rows, int64_t cols) {
+    t = at::empty({rows, cols}, like.options());
+    p = t.data_ptr();
+    ld = cols;
+  }
 };
 Rows rows_arg(PyObject* o, const char* name, at::ScalarType type, int dev, int64_t rows, int64_t cols) {
   Rows r;
@@ -102,15 +107,6 @@ Rows rows_arg(PyObject* o, const char* name, at::ScalarType type, int dev, int64
   r.t = checked(o, name, type, dev);
   r.ld = row_stride(r.t, name, rows, cols);
   r.p = r.t.data_ptr();
-  return r;
-}
-Rows rows_out(PyObject* o, const char* name, const at::Tensor& like, int dev, int64_t rows, int64_t cols, bool make) {
-  Rows r = rows_arg(o, name, like.scalar_type(), dev, rows, cols);
-  if (o == Py_None && make) {
-    r.t = at::empty({rows, cols}, like.options());
-    r.p = r.t.data_ptr();
-    r.ld = cols;
-  }
   return r;
 }
 
@@ -132,33 +128,37 @@ struct Stream {
 };
 
 struct Scratch {
-  at::Tensor t;
+  at::Tensor t;   // given (undefined: made here)
   void* p = nullptr;
   size_t n = 0;
-};
-Scratch scratch(PyObject* o, size_t bytes, const at::Tensor& like, int dev) {
-  Scratch s;
-  if (o == Py_None) {
-    s.t = at::empty({(int64_t)((bytes + 3) / 4)}, like.options().dtype(at::kFloat));
-  } else {
-    s.t = cuda_tensor(o, "ws");
-    if (s.t.get_device() != dev || !s.t.is_contiguous())
-      throw Bad{PyExc_ValueError, "ws: a contiguous tensor on cuda:" + std::to_string(dev) + " is required"};
+  void take(size_t bytes, const at::Tensor& like) {
+    if (!t.defined()) t = at::empty({(int64_t)((bytes + 3) / 4)}, like.options().dtype(at::kFloat));
+    p = t.data_ptr();
+    n = t.nbytes();
   }
-  s.p = s.t.data_ptr();
-  s.n = s.t.nbytes();
+};
+Scratch scratch_arg(PyObject* o, int dev) {
+  Scratch s;
+  if (o == Py_None) return s;
+  s.t = cuda_tensor(o, "ws");
+  if (s.t.get_device() != dev || !s.t.is_contiguous())
+    throw Bad{PyExc_ValueError, "ws: a contiguous tensor on cuda:" + std::to_string(dev) + " is required"};
   return s;
 }
 
-int32_t status_of(PyObject* o, int dev, void** p) {
-  *p = nullptr;
-  if (o != Py_None) {
-    const at::Tensor& t = checked(o, "status_word", at::kInt, dev);
-    if (!t.is_contiguous()) throw Bad{PyExc_ValueError, "status_word: must be contiguous"};
-    *p = t.data_ptr();
-  }
-  return 0;
+int32_t* status_of(PyObject* o, int dev) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = checked(o, "status_word", at::kInt, dev);
+  if (!t.is_contiguous()) throw Bad{PyExc_ValueError, "status_word: must be contiguous"};
+  return static_cast<int32_t*>(t.data_ptr());
 }
+
+// Other Python threads run while this one allocates and launches: either may wait (for the driver, or
+// for room in the stream's queue).  Nothing of Python is touched in its scope.
+struct NoGil {
+  PyThreadState* state = PyEval_SaveThread();
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
 
 int dtype_of(const at::Tensor& x, bool fp32) {
   switch (x.scalar_type()) {
@@ -188,6 +188,8 @@ PyObject* result(int status, std::initializer_list<std::pair<PyObject*, const at
   }
   return r;
 }
+
+float* f32_of(const at::Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; }
 
 bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
 
@@ -227,19 +229,25 @@ PyObject* norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int dev = x.get_device(), dt = dtype_of(x, true), kind = (int)whole(a[3]);
   const int64_t T = x.size(0), d = x.size(1), ldx = row_stride(x, "x", T, d);
   const Stream stream(a[7], dev);
-  void* w = flat(a[1], "w", at::kFloat, dev, {d});
-  void* b = flat(a[2], "b", at::kFloat, dev, {d});
-  const Rows y = rows_out(a[5], "y", x, dev, T, d, true);
+  float* w = static_cast<float*>(flat(a[1], "w", at::kFloat, dev, {d}));
+  float* b = static_cast<float*>(flat(a[2], "b", at::kFloat, dev, {d}));
+  Rows y = rows_arg(a[5], "y", x.scalar_type(), dev, T, d);
+  const bool make_y = a[5] == Py_None, stats = truth(a[6]);
+  const float eps = (float)number(a[4]);
+  const auto call = g_calls.norm;
   at::Tensor mean, rstd;
-  if (truth(a[6])) {
-    const auto o = x.options().dtype(at::kFloat);
-    rstd = at::empty({T}, o);
-    if (kind == MOE_NORM_LAYER) mean = at::empty({T}, o);
+  int st;
+  {
+    NoGil free;
+    if (make_y) y.make(x, T, d);
+    if (stats) {
+      const auto o = x.options().dtype(at::kFloat);
+      rstd = at::empty({T}, o);
+      if (kind == MOE_NORM_LAYER) mean = at::empty({T}, o);
+    }
+    st = call(kind, dt, (int32_t)T, (int32_t)d, x.data_ptr(), ldx, w, b, eps, y.p, y.ld, f32_of(mean), f32_of(rstd),
+              stream.raw);
   }
-  const int st = g_calls.norm(kind, dt, (int32_t)T, (int32_t)d, x.data_ptr(), ldx, static_cast<float*>(w),
-                              static_cast<float*>(b), (float)number(a[4]), y.p, y.ld,
-                              mean.defined() ? mean.data_ptr<float>() : nullptr,
-                              rstd.defined() ? rstd.data_ptr<float>() : nullptr, stream.raw);
   return result(st, {{a[5], &y.t}, {nullptr, &mean}, {nullptr, &rstd}});
   END
 }
@@ -254,20 +262,27 @@ PyObject* norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (a[0] == Py_None) throw Bad{PyExc_TypeError, "dy: a CUDA tensor is required"};
   const Stream stream(a[11], dev);
   const Rows dy = rows_arg(a[0], "dy", type, dev, T, d), dres = rows_arg(a[6], "dres", type, dev, T, d);
-  void* w = flat(a[2], "w", at::kFloat, dev, {d});
-  void* mean = flat(a[3], "mean", at::kFloat, dev, {T});
-  void* rstd = flat(a[4], "rstd", at::kFloat, dev, {T});
-  const Rows dx = rows_out(a[7], "dx", x, dev, T, d, true);
-  const auto f32 = x.options().dtype(at::kFloat);
-  at::Tensor dw, db;
-  if (truth(a[8])) dw = at::empty({d}, f32);
-  if (truth(a[9])) db = at::empty({d}, f32);
+  float* w = static_cast<float*>(flat(a[2], "w", at::kFloat, dev, {d}));
+  float* mean = static_cast<float*>(flat(a[3], "mean", at::kFloat, dev, {T}));
+  float* rstd = static_cast<float*>(flat(a[4], "rstd", at::kFloat, dev, {T}));
+  Rows dx = rows_arg(a[7], "dx", type, dev, T, d);
+  const bool make_dx = a[7] == Py_None, need_dw = truth(a[8]), need_db = truth(a[9]);
   Scratch ws;
-  if (dw.defined() || db.defined()) ws = scratch(a[10], g_calls.norm_workspace((int32_t)T, (int32_t)d), x, dev);
-  const int st = g_calls.norm_backward(kind, dt, (int32_t)T, (int32_t)d, dy.p, dy.ld, x.data_ptr(), ldx,
-                                       static_cast<float*>(w), static_cast<float*>(mean), static_cast<float*>(rstd),
-                                       dres.p, dres.ld, dx.p, dx.ld, dw.defined() ? dw.data_ptr<float>() : nullptr,
-                                       db.defined() ? db.data_ptr<float>() : nullptr, ws.p, ws.n, stream.raw);
+  if (need_dw || need_db) ws = scratch_arg(a[10], dev);
+  const auto call = g_calls.norm_backward;
+  const auto bytes = g_calls.norm_workspace;
+  at::Tensor dw, db;
+  int st;
+  {
+    NoGil free;
+    const auto f32 = x.options().dtype(at::kFloat);
+    if (make_dx) dx.make(x, T, d);
+    if (need_dw) dw = at::empty({d}, f32);
+    if (need_db) db = at::empty({d}, f32);
+    if (need_dw || need_db) ws.take(bytes((int32_t)T, (int32_t)d), x);
+    st = call(kind, dt, (int32_t)T, (int32_t)d, dy.p, dy.ld, x.data_ptr(), ldx, w, mean, rstd, dres.p, dres.ld, dx.p,
+              dx.ld, f32_of(dw), f32_of(db), ws.p, ws.n, stream.raw);
+  }
   return result(st, {{a[7], &dx.t}, {nullptr, &dw}, {nullptr, &db}});
   END
 }
@@ -302,25 +317,28 @@ PyObject* product(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const auto type = p.x.scalar_type();
   const Stream stream(a[11], p.dev);
   const Rows res = rows_arg(a[6], "residual", type, p.dev, p.rows, p.No);
-  const Rows y = rows_out(a[7], "y", p.x, p.dev, p.rows, p.No, true);
-  at::Tensor z;
+  Rows y = rows_arg(a[7], "y", type, p.dev, p.rows, p.No);
   void* zp = flat(a[8], "z", type, p.dev, {p.rows, p.N});
-  if (!zp && a[8] == Py_None && truth(a[9])) {
-    z = at::empty({p.rows, p.N}, p.x.options());
-    zp = z.data_ptr();
-  }
-  void* status;
-  status_of(a[10], p.dev, &status);
+  const bool make_y = a[7] == Py_None, make_z = a[8] == Py_None && truth(a[9]);
+  int32_t* status = status_of(a[10], p.dev);
+  const int64_t E = p.dims.E;
+  const float* bias = static_cast<float*>(p.grouped ? flat(a[3], "bias", at::kFloat, p.dev, {E, p.N})
+                                                    : flat(a[3], "bias", at::kFloat, p.dev, {p.N}));
+  const int32_t* off = p.grouped ? static_cast<int32_t*>(flat(a[2], "offsets", at::kInt, p.dev, {E + 1})) : nullptr;
+  const Calls calls = g_calls;
+  at::Tensor z;
   int st;
-  if (p.grouped) {
-    float* bias = static_cast<float*>(flat(a[3], "bias", at::kFloat, p.dev, {p.dims.E, p.N}));
-    const int32_t* off = static_cast<int32_t*>(flat(a[2], "offsets", at::kInt, p.dev, {p.dims.E + 1}));
-    st = g_calls.grouped(&p.dims, (int32_t)p.rows, p.x.data_ptr(), p.ldx, p.w.data_ptr(), off, bias, y.p, y.ld, zp,
-                         static_cast<int32_t*>(status), stream.raw);
-  } else {
-    float* bias = static_cast<float*>(flat(a[3], "bias", at::kFloat, p.dev, {p.N}));
-    st = g_calls.linear(&p.dims, (int32_t)p.rows, p.x.data_ptr(), p.ldx, p.w.data_ptr(), bias, res.p, res.ld, y.p, y.ld,
-                        zp, static_cast<int32_t*>(status), stream.raw);
+  {
+    NoGil free;
+    if (make_y) y.make(p.x, p.rows, p.No);
+    if (make_z) {
+      z = at::empty({p.rows, p.N}, p.x.options());
+      zp = z.data_ptr();
+    }
+    st = p.grouped ? calls.grouped(&p.dims, (int32_t)p.rows, p.x.data_ptr(), p.ldx, p.w.data_ptr(), off, bias, y.p, y.ld,
+                                   zp, status, stream.raw)
+                   : calls.linear(&p.dims, (int32_t)p.rows, p.x.data_ptr(), p.ldx, p.w.data_ptr(), bias, res.p, res.ld,
+                                  y.p, y.ld, zp, status, stream.raw);
   }
   return result(st, {{a[7], &y.t}, {a[8], &z}});
   END
@@ -341,28 +359,32 @@ PyObject* product_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (a[4] == Py_None) throw Bad{PyExc_ValueError, "z: the forward pass's pre-activation is required with this fn"};
     zp = flat(a[4], "z", type, p.dev, {p.rows, p.N});
   }
-  const Rows dx = rows_out(a[7], "dx", p.x, p.dev, p.rows, p.dims.K, truth(a[9]));
-  at::Tensor dw, db;
+  Rows dx = rows_arg(a[7], "dx", type, p.dev, p.rows, p.dims.K);
   void* dwp = flat(a[8], "dw", type, p.dev, p.w.sizes());
-  if (a[8] == Py_None && truth(a[10])) {
-    dw = at::empty(p.w.sizes(), p.w.options());
-    dwp = dw.data_ptr();
-  }
-  const bool want_db = truth(a[11]);
-  if (want_db) db = at::empty(p.w.sizes().slice(0, p.w.dim() - 1), p.x.options().dtype(at::kFloat));
+  const bool make_dx = a[7] == Py_None && truth(a[9]), make_dw = a[8] == Py_None && truth(a[10]);
+  const bool want_db = truth(a[11]), want_ws = fn != MOE_FN_NONE || want_db;
   Scratch ws;
-  if (fn != MOE_FN_NONE || want_db) ws = scratch(a[12], g_calls.workspace(&p.dims, (int32_t)p.rows), p.x, p.dev);
-  void* status;
-  status_of(a[13], p.dev, &status);
-  float* dbp = want_db ? db.data_ptr<float>() : nullptr;
+  if (want_ws) ws = scratch_arg(a[12], p.dev);
+  int32_t* status = status_of(a[13], p.dev);
+  const int32_t* off =
+      p.grouped ? static_cast<int32_t*>(flat(a[3], "offsets", at::kInt, p.dev, {(int64_t)p.dims.E + 1})) : nullptr;
+  const Calls calls = g_calls;
+  at::Tensor dw, db;
   int st;
-  if (p.grouped) {
-    const int32_t* off = static_cast<int32_t*>(flat(a[3], "offsets", at::kInt, p.dev, {p.dims.E + 1}));
-    st = g_calls.grouped_backward(&p.dims, (int32_t)p.rows, dy.p, dy.ld, p.x.data_ptr(), p.ldx, p.w.data_ptr(), off, zp,
-                                  dx.p, dx.ld, dwp, dbp, ws.p, ws.n, static_cast<int32_t*>(status), stream.raw);
-  } else {
-    st = g_calls.linear_backward(&p.dims, (int32_t)p.rows, dy.p, dy.ld, p.x.data_ptr(), p.ldx, p.w.data_ptr(), zp, dx.p,
-                                 dx.ld, dwp, dbp, ws.p, ws.n, static_cast<int32_t*>(status), stream.raw);
+  {
+    NoGil free;
+    if (make_dx) dx.make(p.x, p.rows, p.dims.K);
+    if (make_dw) {
+      dw = at::empty(p.w.sizes(), p.w.options());
+      dwp = dw.data_ptr();
+    }
+    if (want_db) db = at::empty(p.w.sizes().slice(0, p.w.dim() - 1), p.x.options().dtype(at::kFloat));
+    if (want_ws) ws.take(calls.workspace(&p.dims, (int32_t)p.rows), p.x);
+    st = p.grouped ? calls.grouped_backward(&p.dims, (int32_t)p.rows, dy.p, dy.ld, p.x.data_ptr(), p.ldx, p.w.data_ptr(),
+                                            off, zp, dx.p, dx.ld, dwp, f32_of(db), ws.p, ws.n, status, stream.raw)
+                   : calls.linear_backward(&p.dims, (int32_t)p.rows, dy.p, dy.ld, p.x.data_ptr(), p.ldx,
+                                           p.w.data_ptr(), zp, dx.p, dx.ld, dwp, f32_of(db), ws.p, ws.n, status,
+                                           stream.raw);
   }
   return result(st, {{a[7], &dx.t}, {a[8], &dw}, {nullptr, &db}});
   END
