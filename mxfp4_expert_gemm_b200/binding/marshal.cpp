@@ -191,7 +191,11 @@ PyObject* result(int status, std::initializer_list<std::pair<PyObject*, const at
 
 float* f32_of(const at::Tensor& t) { return t.defined() ? t.data_ptr<float>() : nullptr; }
 
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v == 1;
+}
 
 double number(PyObject* o) {
   const double v = PyFloat_AsDouble(o);

@@ -35,3 +35,9 @@ def test_other_threads_run_while_a_call_is_in_the_library():
     assert t1 - t0 >= 0.9
     assert len([s for s in seen if t0 + 0.1 < s < t1 - 0.1]) >= 10
     assert bool((moe.moe_norm(x, w) - 1 / (1 + 1e-5) ** 0.5).abs().max() < 1e-6)   # the library's own call again
+
+
+def test_a_flag_without_a_truth_value_is_refused():
+    x, w = torch.ones(4, 64, device="cuda"), torch.ones(64, device="cuda")
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        moe.moe_norm(x, w, want_stats=torch.ones(2))
