@@ -522,7 +522,9 @@ def moe_debug_inject_timeout(enable: bool = True) -> None:
 
 # ----------------------------------------------------------- norms and 16-bit products, with gradients
 # Checks, allocations and the calls themselves are in binding/marshal.cpp.  With `stream`, the tensors
-# and the scratch that a call makes are that stream's, as under torch.cuda.stream(stream).
+# and the scratch that a call makes are that stream's, as under torch.cuda.stream(stream).  No call
+# records a graph for autograd: gradients come from the _backward calls, and a tensor that requires one
+# while gradients are on is named in a warning, once.
 def _handle(stream):
     return None if stream is None else stream.cuda_stream
 

@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -49,6 +50,9 @@ const at::Tensor& cuda_tensor(PyObject* o, const char* name) {
   if (!THPVariable_Check(o)) throw Bad{PyExc_TypeError, str(name) + ": a CUDA tensor is required"};
   const at::Tensor& t = THPVariable_Unpack(o);
   if (!t.is_cuda()) throw Bad{PyExc_TypeError, str(name) + ": a CUDA tensor is required"};
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    TORCH_WARN_ONCE(name, " requires a gradient, but this call records no graph: its gradient comes from the _backward "
+                    "call of the same name (with gradients off, as under torch.no_grad(), there is no such warning)");
   return t;
 }
 
