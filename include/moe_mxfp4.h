@@ -473,7 +473,9 @@ size_t moe_linear_workspace_bytes(const moe_linear_dims* dims, int32_t rows);
  * exits, and the workspace status word records MOE_ERR_TIMEOUT (y of that call is then
  * unspecified).  The product calls (moe_linear, moe_grouped_linear and their backward passes)
  * take the hook in the same way, in their first product kernel, and record the timeout in their
- * status_word.  The hook clears itself after that call; nothing faults or hangs. */
+ * status_word; one without a pipeline (a dense forward product of a few rows, a backward call
+ * for db alone) clears it and runs as usual.  The hook clears itself after that call; nothing
+ * faults or hangs. */
 void moe_debug_inject_timeout(int32_t enable);
 
 #ifdef __cplusplus

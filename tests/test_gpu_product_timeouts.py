@@ -61,3 +61,17 @@ def test_timeout_ends_and_the_next_call_is_whole(name):
         for a, b in zip(call(st), want):
             assert torch.equal(a, b)
     assert moe.moe_device_status(st) == moe.MOE_OK
+
+
+def test_calls_without_a_pipeline_clear_the_hook():
+    g = generator(5)
+    x, w, dy = normal(g, 4, 256), normal(g, 512, 256), normal(g, 4, 512)
+    big, st = normal(g, 40, 256), torch.zeros(4, dtype=torch.int32, device="cuda")
+    want, db = moe.moe_linear(x, w), moe.moe_linear_backward(dy, x, w, need_db=True)[2]
+    for call, ref in ((lambda: moe.moe_linear(x, w, status_word=st), want),
+                      (lambda: moe.moe_linear_backward(dy, x, w, need_dx=False, need_dw=False, need_db=True,
+                                                       status_word=st)[2], db)):
+        moe.moe_debug_inject_timeout()
+        assert torch.equal(call(), ref)
+        moe.moe_linear(big, w, status_word=st)
+        assert moe.moe_device_status(st) == moe.MOE_OK
