@@ -752,9 +752,11 @@ int backward_vec(const NormArgs& a) {
   int n = 1;
   if (g) {
     const int y = g == 32 ? 8 : 1;   // short rows: a warp each, eight groups to a block
-    // several rows at a time, and copies ahead, once every resident block has eight steps to take
-    // (the larger code is cold until then; copies of 4 bytes ran slower than loads)
-    const int64_t fit = (int64_t)multiprocessors() * std::max(1, (VEC < 4 ? 1024 : 576) / (g * y));
+    // several rows at a time, and copies ahead, once every block has eight steps to take (the larger
+    // code is cold until then; copies of 4 bytes ran slower than loads).  Blocks: those that are
+    // resident at once, at most kMaxPartialRows.
+    const int64_t fit = std::min<int64_t>(kMaxPartialRows,
+                                          (int64_t)multiprocessors() * std::max(1, (VEC < 4 ? 1024 : 576) / (g * y)));
     const bool many = D > 0 && a.T >= 8 * R * fit * y;
     const int64_t rows = y * (many ? R : 1);
     p.blocks = (int)std::min(std::min<int64_t>((a.T + rows - 1) / rows, fit), norm_partial_rows(a.T, a.d));

@@ -112,3 +112,11 @@ def test_large_products_over_their_residual(fn):
     moe.moe_linear(x, w, fn=fn, residual=y, y=y)
     assert torch.equal(y, want)
     assert torch.equal(buf[:, :8], before[:, :8]) and torch.equal(buf[:, 8 + No:], before[:, 8 + No:])
+
+
+@pytest.mark.parametrize("d,dt", [(768, BF), (1024, HF), (384, SF)])
+def test_norm_backward_at_the_most_blocks(d, dt):
+    """Rows of two warps: more blocks fit than write partial sums (592), and the rows at which each has
+    eight steps of two rows follow from those."""
+    for T in (16 * 592 - 1, 16 * 592 + 1):
+        norms.test_norm(T, d, "layer", dt)
