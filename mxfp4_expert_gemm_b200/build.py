@@ -38,9 +38,12 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def dependencies():
+    return sources() + [f for d, p in ((CSRC, "*.cuh"), (CSRC, "*.h"), (INCLUDE, "*.h")) for f in glob.glob(os.path.join(d, p))]
+
+
 def _deps_mtime() -> float:
-    files = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-    return max(os.path.getmtime(f) for f in files)
+    return max(os.path.getmtime(f) for f in dependencies())
 
 
 def up_to_date(lib: str = LIB) -> bool:

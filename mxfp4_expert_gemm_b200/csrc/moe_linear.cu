@@ -22,13 +22,14 @@
 #include "linear_ptx.cuh"
 #include "moe_linear.cuh"
 #include "packed_math.cuh"
+#include "row_blocks.h"
 
 namespace moe {
 namespace {
 
 constexpr uint64_t kWaitNs = 2000000000ull;   // 2 s: a stuck pipeline, not a slow one
 constexpr uint64_t kLandNs = 20000000ull;     // 20 ms: copies issued before a timeout have landed
-constexpr int kBK = 64;                       // contraction values per stage (a 128-byte row)
+constexpr int kBK = kBlockRows;                // contraction values per stage (a 128-byte row)
 
 struct LinParams {
   int32_t rows, E, fn;
@@ -40,6 +41,7 @@ struct LinParams {
   int32_t nw_max;        // widest tile along j
   int32_t n_jt;          // kWeightGrad: tiles along j
   int32_t splits;        // CTAs of a cluster that share one tile's contraction
+  int32_t win;           // kWeightGrad: rows of map 0's window
   float limit;
   const int32_t* offsets;
   uint16_t* out;
@@ -378,12 +380,16 @@ __device__ __forceinline__ LinTile table_tile(const LinParams& p, const RowTable
   return t;
 }
 
-// Token rows c .. c + 63 of a weight gradient's contraction block as coordinates (d1, d2) of
-// the rank-3 view [rows][64][values] whose two row axes share one stride: row d1 + d2, and d1
-// outside [0, 64) reads zeros.  A block of n < 64 rows is loaded with 64 - n rows of zeros in
-// front (d1 starts at n - 64), so no row of another expert (its values may be infinite) enters
-// the sum; both operands shift alike, and the order of c does not matter.
-__device__ __forceinline__ int tail_shift(int n) { return n < kBK ? n - kBK : 0; }
+// The tensor maps of a weight gradient's operands beside the first (row_blocks.h): windows of 8 rows
+// and of one.
+struct TailMaps {
+  CUtensorMap a[2], b[2];
+};
+// Blocks of 64 along a tile's contraction.
+template <int MODE>
+__device__ __forceinline__ int tile_blocks(const LinParams& p, const LinTile& t) {
+  return MODE == kWeightGrad ? weight_blocks(p.win, t.c0, t.clen) : (t.clen + kBK - 1) / kBK;
+}
 
 // ------------------------------------------------------------------------------ epilogue
 // Four warps (128 threads, named barrier `bar`) finish 32 columns of a tile, held as matrix
@@ -639,7 +645,7 @@ struct SplitCfg {
 template <int MODE, bool SW, int NB, bool BF>
 __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB>::CPS)
     lin_split_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
-                     const LinParams p) {
+                     const __grid_constant__ TailMaps tails, const LinParams p) {
   using C = SplitCfg<MODE, NB>;
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
   pdl_wait();   // dz, in a backward call; what came before the call is complete without it
   const uint32_t tmem = *s_tmem;
   const LinTile t = *s_tile;
-  const int kb_all = t.ok ? (t.clen + kBK - 1) / kBK : 0;
+  const int kb_all = t.ok ? tile_blocks<MODE>(p, t) : 0;
   const int kb0 = (int)((int64_t)rank * kb_all / S), kb1 = (int)((int64_t)(rank + 1) * kb_all / S);
 
   if (warp == 0) {
@@ -714,10 +720,12 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
           for (int h = 0; h < 2; ++h) ptx::tma_load_3d(a + h * 8192, &tm_a, t.i0 + 64 * h, c, t.e, &full[s]);
         }
         if (MODE == kWeightGrad) {
-          const int d1 = tail_shift(t.clen - c), d2 = t.c0 + c;
+          const RowBlock r = weight_block(p.win, t.c0, t.clen, kb);
+          const CUtensorMap* map_a = r.map == 0 ? &tm_a : &tails.a[r.map - 1];
+          const CUtensorMap* map_b = r.map == 0 ? &tm_b : &tails.b[r.map - 1];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) ptx::tma_load_3d(a + h * 8192, &tm_a, t.i0 + 64 * h, d1, d2, &full[s]);
-          ptx::tma_load_3d(b, &tm_b, t.j0, d1, d2, &full[s]);
+          for (int h = 0; h < 2; ++h) ptx::tma_load_3d(a + h * 8192, map_a, t.i0 + 64 * h, r.d1, r.d2, &full[s]);
+          ptx::tma_load_3d(b, map_b, t.j0, r.d1, r.d2, &full[s]);
         } else {
           ptx::tma_load_2d(b, &tm_b, c, t.j0, &full[s]);
         }
@@ -909,7 +917,8 @@ struct PairCfg {
 
 template <int MODE, bool SW, bool BF>
 __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
-    lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ BMaps tm_b, const LinParams p) {
+    lin_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ BMaps tm_b,
+                    const __grid_constant__ TailMaps tails, const LinParams p) {
   using C = PairCfg<MODE>;
   pdl_trigger();
   extern __shared__ uint8_t smem_raw[];
@@ -965,7 +974,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     bool stop = false, withheld = false;
     for (uint32_t item = unit0; item < n_items && !stop; item += units) {
       const LinTile t = table_tile<MODE>(p, tab, item, C::STEP, kIW);
-      const int kb_all = (t.clen + kBK - 1) / kBK, half = t.nw / 2;
+      const int kb_all = tile_blocks<MODE>(p, t), half = t.nw / 2;
       const int boxes = (half + 31) / 32;   // B's rows in units of 32, as one copy
       const bool narrow = half <= 64;       // (kWeightGrad: one or two 64-wide copies)
       const uint32_t bytes = 2 * (C::A_PANEL + (MODE != kWeightGrad ? 4096 * boxes : narrow ? 8192 : 16384));
@@ -988,7 +997,8 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
           uint8_t* b = a + C::A_PANEL;
           const uint32_t bar = ptx::mapa_shared(&full[s], 0);
           const int c = kb * kBK;
-          const int d1 = tail_shift(t.clen - c), d2 = t.c0 + c;   // (kWeightGrad)
+          RowBlock r = {};
+          if (MODE == kWeightGrad) r = weight_block(p.win, t.c0, t.clen, kb);
           if (is_a) {
             if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], bytes);
             if (MODE == kForward) {
@@ -998,12 +1008,13 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 if (MODE == kInputGrad) ptx::tma_load_3d_pair(a + h * 8192, &tm_a, i0 + 64 * h, c, t.e, bar);
-                else ptx::tma_load_3d_pair(a + h * 8192, &tm_a, i0 + 64 * h, d1, d2, bar);
+                else ptx::tma_load_3d_pair(a + h * 8192, r.map == 0 ? &tm_a : &tails.a[r.map - 1], i0 + 64 * h, r.d1, r.d2, bar);
               }
             }
           } else if (MODE == kWeightGrad) {
-            ptx::tma_load_3d_pair(b, map_b, j0, d1, d2, bar);
-            if (!narrow) ptx::tma_load_3d_pair(b + 8192, map_b, j0 + 64, d1, d2, bar);
+            const CUtensorMap* map = r.map == 0 ? map_b : &tails.b[r.map - 1];
+            ptx::tma_load_3d_pair(b, map, j0, r.d1, r.d2, bar);
+            if (!narrow) ptx::tma_load_3d_pair(b + 8192, map, j0 + 64, r.d1, r.d2, bar);
           } else {
             ptx::tma_load_2d_pair(b, map_b, c, j0, bar);
           }
@@ -1036,7 +1047,7 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
       bool stop = false;
       for (uint32_t item = unit0; item < n_items && !stop; item += units, ++li) {
         const LinTile t = table_tile<MODE>(p, tab, item, C::STEP, kIW);
-        const int kb_all = (t.clen + kBK - 1) / kBK, b2 = li & 1;
+        const int kb_all = tile_blocks<MODE>(p, t), b2 = li & 1;
         const uint32_t idesc = ptx::idesc_f16(BF, 256, t.nw, C::A_MN, C::B_MN);
         if (li >= 2 && !__all_sync(0xffffffffu, ptx::mbar_wait_cluster_bounded(
                                                     &acce[b2], (uint32_t)((li >> 1) - 1) & 1, s_abort, kWaitNs)))
@@ -1268,6 +1279,22 @@ bool map16(CUtensorMap* m, bool bf16, const void* base, int rank, uint64_t d0, u
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map `map` of a weight gradient's operand.
+bool row_windows(CUtensorMap* m, bool bf16, const void* base, uint64_t values, int32_t rows, int64_t ld, int map) {
+  const uint64_t w = window_rows(map, rows);
+  return map16(m, bf16, base, 3, values, w, ld, (uint64_t)rows - w + 1, ld, kBK);
+}
+// (A dense product's only tail ends with the buffer: map 0 serves it.)
+bool tail_maps(const LinArgs& a, TailMaps* t) {
+  if (a.mode != kWeightGrad || !a.offsets) return true;
+  const bool bf = a.bf16 != 0;
+  for (int k = 0; k < 2; ++k)
+    if (!row_windows(&t->a[k], bf, a.other, a.K, a.rows, a.ld_other, k + 1) ||
+        !row_windows(&t->b[k], bf, a.tok, a.N, a.rows, a.ld_tok, k + 1))
+      return false;
+  return true;
+}
+
 // The map of A: 128 rows per copy of a K-major one (SwiGLU: 64 gate and the 64 matching up
 // rows), 64 x 64 boxes of an MN-major one.
 bool a_map(const LinArgs& a, CUtensorMap* m) {
@@ -1280,8 +1307,8 @@ bool a_map(const LinArgs& a, CUtensorMap* m) {
       return map16(m, bf, a.other, 2, K, E * N, K, 1, 0, 128);   // W [E * N][K]
     case kInputGrad:   // W [E][N][K] (rows past an expert's N read zeros)
       return map16(m, bf, a.other, 3, K, N, K, E, N * K, 64);
-    default:           // x as [rows][64][K]: see tail_shift
-      return map16(m, bf, a.other, 3, K, 64, a.ld_other, rows, a.ld_other, 64);
+    default:
+      return row_windows(m, bf, a.other, K, a.rows, a.ld_other, 0);
   }
 }
 
@@ -1289,8 +1316,7 @@ bool a_map(const LinArgs& a, CUtensorMap* m) {
 bool b_map(const LinArgs& a, uint32_t box, CUtensorMap* m) {
   const bool bf = a.bf16 != 0;
   const uint64_t rows = a.rows;
-  if (a.mode == kWeightGrad)   // dz as [rows][64][N]
-    return map16(m, bf, a.tok, 3, (uint64_t)a.N, 64, a.ld_tok, rows, a.ld_tok, 64);
+  if (a.mode == kWeightGrad) return row_windows(m, bf, a.tok, (uint64_t)a.N, a.rows, a.ld_tok, 0);
   return map16(m, bf, a.tok, 2, (uint64_t)(a.mode == kForward ? a.K : a.N), rows, a.ld_tok, 1, 0, box);
 }
 
@@ -1317,6 +1343,7 @@ LinParams params_of(const LinArgs& a, int iw) {
   p.J = a.N;
   p.C = a.mode == kForward ? a.K : a.N;
   p.a_rows = a.N;
+  p.win = window_rows(0, a.rows);
   p.n_it = (p.I + iw - 1) / iw;
   p.offsets = a.offsets;
   p.out = static_cast<uint16_t*>(a.out);
@@ -1345,7 +1372,8 @@ template <int MODE, bool SW, int NB, bool BF>
 int launch_split_of(const LinArgs& a) {
   using C = SplitCfg<MODE, NB>;
   CUtensorMap ma, mb;
-  if (!a_map(a, &ma) || !b_map(a, NB, &mb)) return -1;
+  TailMaps tails = {};
+  if (!a_map(a, &ma) || !b_map(a, NB, &mb) || !tail_maps(a, &tails)) return -1;
   LinParams p = params_of(a, SW ? 64 : 128);
   p.nw_max = NB;
   p.n_jt = (a.N + NB - 1) / NB;
@@ -1364,8 +1392,8 @@ int launch_split_of(const LinArgs& a) {
   if (grid > 0x7fffffff) return -1;
   const dim3 g((unsigned)grid), b(C::THREADS);
   const cudaError_t err = p.splits == 1
-      ? launch_kernel(kern, g, b, C::SMEM, a.stream, a.pdl != 0, ma, mb, p)
-      : launch_kernel_cluster(kern, g, b, C::SMEM, a.stream, a.pdl != 0, (unsigned)p.splits, ma, mb, p);
+      ? launch_kernel(kern, g, b, C::SMEM, a.stream, a.pdl != 0, ma, mb, tails, p)
+      : launch_kernel_cluster(kern, g, b, C::SMEM, a.stream, a.pdl != 0, (unsigned)p.splits, ma, mb, tails, p);
   return err == cudaSuccess ? 1 : -1;
 }
 
@@ -1419,7 +1447,8 @@ int launch_pair_of(const LinArgs& a) {
   using C = PairCfg<MODE>;
   CUtensorMap ma;
   BMaps mb;
-  if (!a_map(a, &ma)) return -1;
+  TailMaps tails = {};
+  if (!a_map(a, &ma) || !tail_maps(a, &tails)) return -1;
   for (uint32_t m = 0; m < (MODE == kWeightGrad ? 1 : 4); ++m)
     if (!b_map(a, 32 * (m + 1), &mb.m[m])) return -1;
   LinParams p = params_of(a, SW ? 128 : 256);
@@ -1434,7 +1463,8 @@ int launch_pair_of(const LinArgs& a) {
   p.n_jt = (a.N + p.nw_max - 1) / p.nw_max;
   const int64_t tiles = (MODE == kWeightGrad ? (int64_t)a.E * p.n_jt : row_tiles_bound(a, p.nw_max)) * p.n_it;
   const unsigned grid = 2 * (unsigned)std::min<int64_t>(tiles, n);
-  return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, a.pdl != 0, 2u, ma, mb, p) ==
+  return launch_kernel_cluster(kern, dim3(grid), dim3(C::THREADS), C::SMEM, a.stream, a.pdl != 0, 2u, ma, mb, tails,
+                               p) ==
                  cudaSuccess ? 1 : -1;
 }
 
