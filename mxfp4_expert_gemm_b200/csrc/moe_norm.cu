@@ -469,12 +469,14 @@ __global__ void __launch_bounds__(VEC < 4 ? 1024 : 576) norm_backward_kernel(con
       if (D > 0) return *reinterpret_cast<const Pack<DT, VEC>*>(slot(stage, i, k, t));
       return t == 0 ? xv[i][k] : t == 1 ? dv[i][k] : rv[i][k];
     };
-    float mr[R], r[R], c[2 * R];   // xh = x r - m r
+    // xh = (x - m) r, the mean subtracted first: x r - m r is off by 2^-24 of |m| r, which counts in
+    // rows whose mean is far from their spread, and where the terms of dx cancel
+    float m[R], r[R], c[2 * R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int64_t row = min(row0 + i, (int64_t)p.T - 1);
       r[i] = rn[i];
-      mr[i] = mn[i] * r[i];
+      m[i] = mn[i];
       c[i] = c[R + i] = 0.f;
       if (D == 0) {
 #pragma unroll
@@ -499,7 +501,8 @@ __global__ void __launch_bounds__(VEC < 4 ? 1024 : 576) norm_backward_kernel(con
             float x[VEC], dy[VEC], g[VEC];
             unpack<DT, VEC>(get(i, k, 0), x);
             unpack<DT, VEC>(get(i, k, 1), dy);
-            vfma(x, x, r[i], -mr[i]);           // xh
+            if (LAYER) vfma(x, x, 1.f, -m[i]);
+            vfma(x, x, r[i], 0.f);              // xh
             vmul(g, dy, w[k]);
             vfma(s1, g, x, s1);
             vfma(aw[k], dy, x, aw[k]);
@@ -537,9 +540,10 @@ __global__ void __launch_bounds__(VEC < 4 ? 1024 : 576) norm_backward_kernel(con
             float x[VEC], dy[VEC];
             unpack<DT, VEC>(get(i, k, 0), x);
             unpack<DT, VEC>(get(i, k, 1), dy);
-            // r (g - xh mean(g xh) - mean(g)), xh = x r - m r
+            // r g - r mean(g) - (x - m) r r mean(g xh)
+            if (LAYER) vfma(x, x, 1.f, -m[i]);
             vmul(dy, dy, w[k]);
-            vfma(dy, dy, r[i], fmaf(-mr[i], c1, c2));
+            vfma(dy, dy, r[i], c2);
             vfma(dy, x, c1 * r[i], dy);
             if (p.dres) {
               unpack<DT, VEC>(get(i, k, 2), x);
