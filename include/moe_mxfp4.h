@@ -441,7 +441,8 @@ moe_status moe_linear(const moe_linear_dims* dims, int32_t M, const void* x, int
  * != NONE; NULL otherwise):  dz = dy * f'(z) (a clamp passes the gradient up to and at its
  * bound; RELU at 0: 0),  dx = dz W [M][K],  dw = dz^T x [N][K],  db = column sums of dz [N]
  * fp32.  The residual's gradient is dy itself.  dx, dw, db: NULL to skip.  dz enters the
- * products rounded to dtype (the tensor cores' operand type); db sums it unrounded.
+ * products rounded to dtype (the tensor cores' operand type; in fp16 a dz past 65504 becomes
+ * infinite); db sums it unrounded.
  * ws: moe_linear_workspace_bytes(dims, M) bytes, 16-byte aligned.  M = 0 writes zeros to dw
  * and db.  x is needed for dw only, w for dx only.  Errors: as moe_linear, MOE_ERR_WORKSPACE. */
 moe_status moe_linear_backward(const moe_linear_dims* dims, int32_t M, const void* dy, int64_t lddy, const void* x,
@@ -464,7 +465,8 @@ moe_status moe_grouped_linear_backward(const moe_linear_dims* dims, int32_t P, c
                                        const void* z, void* dx, int64_t lddx, void* dw, float* db, void* ws,
                                        size_t ws_bytes, int32_t* status_word, void* stream);
 
-/* Workspace of the two backward calls for `rows` rows (M or P); 0 for unsupported dims. */
+/* Workspace of the two backward calls for `rows` rows (M or P), db among the results or not; 0
+ * for unsupported dims. */
 size_t moe_linear_workspace_bytes(const moe_linear_dims* dims, int32_t rows);
 
 /* Test hook for the device-side failure path.  With enable != 0, the next moe_forward

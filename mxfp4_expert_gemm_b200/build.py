@@ -13,8 +13,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_mxfp4.so")
-# The same library with every store at a computed offset checked against its buffer
-# (-DMOE_DEBUG_BOUNDS): an out-of-range store is skipped and MOE_ERR_BOUNDS recorded.
+# The same library with the layer's and the tiled products' stores at computed offsets checked against
+# their buffers (-DMOE_DEBUG_BOUNDS): an out-of-range store is skipped and MOE_ERR_BOUNDS recorded.
 LIB_BOUNDS = os.path.join(PKG, "libmoe_mxfp4_bounds.so")
 # The tensor-argument part of the binding (compiled against this torch and Python, named by them).
 MARSHAL_SRC = os.path.join(PKG, "binding", "marshal.cpp")

