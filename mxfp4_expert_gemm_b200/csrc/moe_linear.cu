@@ -677,18 +677,21 @@ __global__ void __launch_bounds__(SplitCfg<MODE, NB>::THREADS, SplitCfg<MODE, NB
     ptx::prefetch_tensormap(&tm_a);
     ptx::prefetch_tensormap(&tm_b);
   }
+  if (warp == 2) {
+    const LinTile t = find_tile<MODE>(p, item, 16, SW ? 64 : 128);
+    if (lane == 0) *s_tile = t;
+  }
+  // dz, in a backward call; what came before the call is complete without it.  Tensor memory is taken
+  // after the wait: a CTA that held some while it waits for its predecessor could keep it from a CTA of
+  // another stream whose own successor holds what that predecessor needs, and taking it has no bound.
+  pdl_wait();
   if (warp == 1) {
     ptx::tmem_alloc(s_tmem, C::TMEM_COLS);
     ptx::tmem_relinquish();
     ptx::tc_fence_before();
   }
-  if (warp == 2) {
-    const LinTile t = find_tile<MODE>(p, item, 16, SW ? 64 : 128);
-    if (lane == 0) *s_tile = t;
-  }
   __syncthreads();
   ptx::tc_fence_after();
-  pdl_wait();   // dz, in a backward call; what came before the call is complete without it
   const uint32_t tmem = *s_tmem;
   const LinTile t = *s_tile;
   const int kb_all = t.ok ? tile_blocks<MODE>(p, t) : 0;
@@ -953,15 +956,15 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
     ptx::prefetch_tensormap(&tm_a);
     for (int m = 0; m < (MODE == kWeightGrad ? 1 : 4); ++m) ptx::prefetch_tensormap(&tm_b.m[m]);
   }
+  build_table<MODE>(p, tab, C::STEP);
+  pdl_wait();   // (as in the split kernel, before the tensor memory)
   if (warp == 1) {
     ptx::tmem_alloc_pair(s_tmem, 512);
     ptx::tmem_relinquish_pair();
     ptx::tc_fence_before();
   }
-  build_table<MODE>(p, tab, C::STEP);
   ptx::cluster_sync();   // the peer's copies, commits and arrivals find initialized barriers
   ptx::tc_fence_after();
-  pdl_wait();   // (as in the split kernel)
   const uint32_t tmem = *s_tmem;
   const uint32_t n_items = tab->items;
 
