@@ -270,6 +270,11 @@ __global__ void __launch_bounds__(MxCfg<BN, NP, S, CPS, EG, NPW, TERMS, FP4, CG>
       ptx::prefetch_tensormap(&tm_sfa);
     }
   }
+  // Everything above overlaps the previous kernel; the work list is its output.  Tensor memory is taken
+  // after the wait, which has no bound: a pair (all 512 columns) and a small-batch CTA fit on one SM, and
+  // layers of both paths on two streams could each hold, while they wait, what the kernel that the other
+  // waits for needs.
+  pdl_wait();
   if (warp == C::MMA_WARP) {
     if (CG == 2) {
       ptx::tmem_alloc_pair(s_tmem, C::TMEM_COLS);
@@ -285,8 +290,6 @@ __global__ void __launch_bounds__(MxCfg<BN, NP, S, CPS, EG, NPW, TERMS, FP4, CG>
   else __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  // Everything above overlaps the previous kernel; the work list is its output.
-  pdl_wait();
   const int n_units = *p.ntiles * p.n_ru;
   const int ksplit = choose_ksplit(n_units, unit_stride, p.ksplit_max);   // same in every CTA
   const int n_items = n_units * ksplit;

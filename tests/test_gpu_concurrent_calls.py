@@ -7,7 +7,9 @@ import pytest
 import torch
 
 import mxfp4_expert_gemm_b200 as moe
+from _gpu_case import case
 from _train_ref import generator, normal
+from test_gpu_parity import SMALL
 
 pytestmark = [pytest.mark.gpu, pytest.mark.timeout(120)]
 
@@ -84,3 +86,20 @@ def _run(calls, graphed, own, rounds, seed):
 
 def test_norms_and_products():
     _run(_operators(generator(1)), {0: 0, 1: 3, 2: 5, 3: 9}, {}, 40, 1)
+
+
+def test_layers_of_both_paths_beside_them():
+    """The MXFP4 layer's two paths on streams of their own, and the other calls around them."""
+    c = case(SMALL["mid_ragged"])
+    cfg, layers = c["cfg"], []
+    for path in ("gemm", "gemv", "gemm", "gemv"):
+        dims = moe.make_dims(cfg.d, cfg.I, cfg.E, cfg.k, cfg.rms_eps, cfg.swiglu_limit, path=path)
+        ws = moe.new_workspace(dims, cfg.T)
+
+        def layer(s=None, dims=dims, ws=ws):
+            with torch.cuda.stream(s or torch.cuda.current_stream()):
+                return [moe.moe_forward(dims, c["x_dev"], c["gamma_dev"], c["rw_dev"], c["rb_dev"], *c["W"]["gpu"], ws)]
+        layers.append(layer)
+    calls = _operators(generator(2))
+    n = len(calls)
+    _run(calls + layers, {2: 3}, {0: n, 1: n + 1, 2: n + 2, 3: n + 3}, 40, 2)
