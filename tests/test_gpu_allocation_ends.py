@@ -112,3 +112,25 @@ def test_norms(T, d, dt, end):
     assert torch.equal(moe.moe_norm(px, pw, p(b), kind="layer", y=p(torch.zeros_like(x))), y)
     _same(moe.moe_norm_backward(p(dy), px, pw, p(mean), p(rstd), kind="layer", dres=p(r), dx=p(torch.zeros_like(x))), back)
     assert p.intact()
+
+
+LOW, HIGH = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("fn", ["none", "swiglu"])
+@pytest.mark.parametrize("offs", [
+    [0, HIGH, LOW, 20], [LOW, LOW, LOW, LOW], [HIGH] * 4, [60, 40, 20, 0], [0, 63, 62, 63], [5, 5, 64, 63], [0, 0, 0, 64]])
+def test_offsets_out_of_range_or_order(offs, fn):
+    """Reported, and nothing beside the outputs is touched."""
+    g = generator(4)
+    P, K, N, E = 63, 72, 144, 3
+    No = N // 2 if fn == "swiglu" else N
+    off, p = torch.tensor(offs, dtype=torch.int32, device="cuda"), Place(True)
+    x, w, dy, z = p(normal(g, P, K)), p(normal(g, E, N, K)), p(normal(g, P, No)), p(normal(g, P, N))
+    y, dx, dw = p(torch.zeros_like(dy)), p(torch.zeros_like(x)), p(torch.zeros_like(w))
+    st = torch.zeros(4, dtype=torch.int32, device="cuda")
+    moe.moe_grouped_linear(x, w, off, fn=fn, y=y, status_word=st)
+    assert moe.moe_device_status(st) == moe.MOE_ERR_INVALID_ARG
+    moe.moe_grouped_linear_backward(dy, x, w, off, z if fn != "none" else None, fn=fn, dx=dx, dw=dw, need_db=True, status_word=st)
+    assert moe.moe_device_status(st) == moe.MOE_ERR_INVALID_ARG
+    assert p.intact()
