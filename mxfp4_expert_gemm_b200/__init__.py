@@ -235,6 +235,19 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(stream, shape, dtype, device) -> torch.Tensor:
+    """An output of a call on `stream`, of that stream's memory (a block that another stream freed may
+    still be in use there, and would go back there while this one writes it)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _empty_like(stream, x) -> torch.Tensor:
+    return _empty(stream, x.shape, x.dtype, x.device)
+
+
 def _check(st: int, what: str):
     if st != MOE_OK:
         raise MoeError(st, what)
@@ -282,9 +295,9 @@ def moe_mxfp4_quantize(w: torch.Tensor, codes: torch.Tensor | None = None, scale
     E, N, K = w.shape
     cs, ss = mxfp4_shapes(E, N, K)
     if codes is None:
-        codes = torch.empty(cs, dtype=torch.uint8, device=w.device)
+        codes = _empty(stream, cs, torch.uint8, w.device)
     if scales is None:
-        scales = torch.empty(ss, dtype=torch.uint8, device=w.device)
+        scales = _empty(stream, ss, torch.uint8, w.device)
     if codes.numel() != moe_mxfp4_codes_bytes(E, N, K) or scales.numel() != moe_mxfp4_scales_bytes(E, N, K):
         raise ValueError("codes / scales have the wrong size")
     _check(lib().moe_mxfp4_quantize(_ptr(w), E, N, K, role, _ptr(codes), _ptr(scales), _ptr(status_word),
@@ -310,11 +323,11 @@ def moe_route(dims: moe_dims, x, norm_w, router_w, router_b, ws, stream=None):
     _need(x, torch.bfloat16, "x")
     dev = x.device
     k, E = dims.top_k, dims.E
-    out = dict(topk_idx=torch.empty((T, k), dtype=torch.int32, device=dev),
-               topk_w=torch.empty((T, k), dtype=torch.float32, device=dev),
-               counts=torch.empty(E, dtype=torch.int32, device=dev),
-               offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-               perm=torch.empty(T * k, dtype=torch.int32, device=dev))
+    out = dict(topk_idx=_empty(stream, (T, k), torch.int32, dev),
+               topk_w=_empty(stream, (T, k), torch.float32, dev),
+               counts=_empty(stream, E, torch.int32, dev),
+               offsets=_empty(stream, E + 1, torch.int32, dev),
+               perm=_empty(stream, T * k, torch.int32, dev))
     _check(lib().moe_route(ctypes.byref(dims), T, _ptr(x), _ptr(norm_w), _ptr(router_w), _ptr(router_b),
                            _ptr(out["topk_idx"]), _ptr(out["topk_w"]), _ptr(out["counts"]), _ptr(out["offsets"]),
                            _ptr(out["perm"]), _ptr(ws), ws.numel(), _stream(stream)), "moe_route")
@@ -328,12 +341,12 @@ def moe_forward(dims: moe_dims, x, norm_w, router_w, router_b, w1_codes, w1_scal
     _need(x, torch.bfloat16, "x")
     dev = x.device
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty_like(stream, x)
     r = None
     if want_routing:
-        r = dict(topk_idx=torch.empty((T, dims.top_k), dtype=torch.int32, device=dev),
-                 topk_w=torch.empty((T, dims.top_k), dtype=torch.float32, device=dev),
-                 counts=torch.empty(dims.E, dtype=torch.int32, device=dev))
+        r = dict(topk_idx=_empty(stream, (T, dims.top_k), torch.int32, dev),
+                 topk_w=_empty(stream, (T, dims.top_k), torch.float32, dev),
+                 counts=_empty(stream, dims.E, torch.int32, dev))
     _check(lib().moe_forward(ctypes.byref(dims), T, _ptr(x), _ptr(norm_w), _ptr(router_w), _ptr(router_b),
                              _ptr(w1_codes), _ptr(w1_scales), _ptr(w2_codes), _ptr(w2_scales), _ptr(y),
                              _ptr(r["topk_idx"]) if r else None, _ptr(r["topk_w"]) if r else None,
@@ -387,12 +400,12 @@ def moe_forward_partial(dims: moe_dims, x, norm_w, router_w, router_b, w1_codes,
     _need(x, torch.bfloat16, "x")
     dev = x.device
     if y_partial is None:
-        y_partial = torch.empty((T, dims.d), dtype=torch.float32, device=dev)
+        y_partial = _empty(stream, (T, dims.d), torch.float32, dev)
     r = None
     if want_routing:
-        r = dict(topk_idx=torch.empty((T, dims.top_k), dtype=torch.int32, device=dev),
-                 topk_w=torch.empty((T, dims.top_k), dtype=torch.float32, device=dev),
-                 counts=torch.empty(dims.E, dtype=torch.int32, device=dev))
+        r = dict(topk_idx=_empty(stream, (T, dims.top_k), torch.int32, dev),
+                 topk_w=_empty(stream, (T, dims.top_k), torch.float32, dev),
+                 counts=_empty(stream, dims.E, torch.int32, dev))
     _check(lib().moe_forward_partial(ctypes.byref(dims), T, _ptr(x), _ptr(norm_w), _ptr(router_w), _ptr(router_b),
                                      _ptr(w1_codes), _ptr(w1_scales), _ptr(w2_codes), _ptr(w2_scales), _ptr(y_partial),
                                      _ptr(r["topk_idx"]) if r else None, _ptr(r["topk_w"]) if r else None,
@@ -406,8 +419,8 @@ def moe_forward_norm(dims: moe_dims, x, norm_w, router_w, router_b, w1_codes, w1
     """(y, y_norm): the layer's output and the next block's RMSNorm of it, in one pass."""
     _need(x, torch.bfloat16, "x")
     _need(next_norm_w, torch.float32, "next_norm_w", (dims.d,))
-    y = torch.empty_like(x) if y is None else y
-    y_norm = torch.empty_like(x) if y_norm is None else y_norm
+    y = _empty_like(stream, x) if y is None else y
+    y_norm = _empty_like(stream, x) if y_norm is None else y_norm
     _check(lib().moe_forward_norm(ctypes.byref(dims), x.shape[0], _ptr(x), _ptr(norm_w), _ptr(router_w),
                                   _ptr(router_b), _ptr(w1_codes), _ptr(w1_scales), _ptr(w2_codes), _ptr(w2_scales),
                                   _ptr(next_norm_w), float(next_eps), _ptr(y), _ptr(y_norm), _ptr(ws), ws.numel(),
@@ -420,9 +433,9 @@ def moe_residual_norm(x, s, norm_w=None, eps=1e-5, y=None, y_norm=None, stream=N
     _need(x, torch.bfloat16, "x")
     _need(s, torch.float32, "s", tuple(x.shape))
     T, d = x.shape
-    y = torch.empty_like(x) if y is None else y
+    y = _empty_like(stream, x) if y is None else y
     if norm_w is not None and y_norm is None:
-        y_norm = torch.empty_like(x)
+        y_norm = _empty_like(stream, x)
     _check(lib().moe_residual_norm(T, d, _ptr(x), _ptr(s), _ptr(norm_w), float(eps), _ptr(y),
                                    _ptr(y_norm) if norm_w is not None else None, _stream(stream)),
            "moe_residual_norm")
@@ -471,7 +484,7 @@ def moe_forward_timed(dims: moe_dims, x, norm_w, router_w, router_b, w1_codes, w
     small batches: route with the grouping, pack, gate_up, down, combine)."""
     _need(x, torch.bfloat16, "x")
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty_like(stream, x)
     arr, n = None, 0
     if events:
         arr = (ctypes.c_void_p * len(events))(*[e.cuda_event for e in events])
@@ -507,7 +520,7 @@ def moe_forward_no_alloc(dims: moe_dims, x, norm_w, router_w, router_b, w1_codes
     torch only when it is not given."""
     _need(x, torch.bfloat16, "x")
     if y is None:
-        y = torch.empty_like(x)
+        y = _empty_like(stream, x)
     _check(lib().moe_forward_no_alloc(ctypes.byref(dims), x.shape[0], _ptr(x), _ptr(norm_w), _ptr(router_w),
                                       _ptr(router_b), _ptr(w1_codes), _ptr(w1_scales), _ptr(w2_codes),
                                       _ptr(w2_scales), _ptr(y), _ptr(status_out), _stream(stream)),
