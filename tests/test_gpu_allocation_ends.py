@@ -134,3 +134,31 @@ def test_offsets_out_of_range_or_order(offs, fn):
     moe.moe_grouped_linear_backward(dy, x, w, off, z if fn != "none" else None, fn=fn, dx=dx, dw=dw, need_db=True, status_word=st)
     assert moe.moe_device_status(st) == moe.MOE_ERR_INVALID_ARG
     assert p.intact()
+
+
+@pytest.mark.parametrize("end", [True, False])
+@pytest.mark.parametrize("act", ["bf16", "mxfp8", "mxfp4"])
+@pytest.mark.parametrize("path", ["gemm", "gemv"])
+@pytest.mark.parametrize("T,d,I,E,k", [(37, 192, 320, 5, 3), (200, 576, 448, 8, 4), (300, 256, 128, 64, 4), (1, 2880, 704, 4, 2)])
+def test_layer(T, d, I, E, k, path, act, end):
+    """The MXFP4 layer with its weights, workspace and tokens so placed."""
+    g = generator(T + d)
+    F = torch.float32
+    x, gamma = normal(g, T, d), normal(g, d, dtype=F, mean=1.0, std=0.1)
+    rw, rb = normal(g, E, d, dtype=F, std=0.1), normal(g, E, dtype=F, std=0.1)
+    w1, w2 = normal(g, E, 2 * I, d, dtype=F, std=d ** -0.5), normal(g, E, d, I, dtype=F, std=I ** -0.5)
+    dims = moe.make_dims(d, I, E, k, path=path, act=act)
+    W = [*moe.moe_mxfp4_quantize(w1, role="gate_up"), *moe.moe_mxfp4_quantize(w2, role="down")]
+    ws = moe.new_workspace(dims, T)
+    want = moe.moe_forward(dims, x, gamma, rw, rb, *W, ws)
+    assert moe.moe_device_status(ws) == moe.MOE_OK
+    p = Place(end)
+    n = ws.numel()
+    pws = p(torch.zeros((n + 255) // 256 * 256, dtype=torch.uint8, device="cuda"))
+    pW = [p(t) for t in W]
+    got = moe.moe_forward(dims, p(x), p(gamma), p(rw), p(rb), *pW, pws, y=p(torch.zeros_like(x)))
+    assert moe.moe_device_status(pws) == moe.MOE_OK
+    assert torch.equal(got, want) and p.intact()
+    q = [p(torch.zeros_like(t)) for t in W[:2]]
+    moe.moe_mxfp4_quantize(p(w1) if w1.numel() * 4 < OWN else w1, *q, role="gate_up")
+    assert torch.equal(q[0], W[0]) and torch.equal(q[1], W[1]) and p.intact()
